@@ -19,6 +19,10 @@ from ._lib import (  # noqa: F401
     layer_prefill_host,
     lib,
     lib_path,
+    linear_decode_step,
+    linear_prefill,
+    linear_prefill_backward,
+    linear_prefill_workspace_size,
     prefill,
     prefill_backward,
     prefill_backward_chunked,
@@ -26,4 +30,8 @@ from ._lib import (  # noqa: F401
     prefill_noalloc,
     prefill_status,
     prefill_workspace_size,
+    state_compact,
+    state_copy,
+    state_fork,
+    state_free,
 )

@@ -67,7 +67,28 @@ SIGNATURES = {
                                         _i32, _f32, _vp, _i32, _vp, _vp, _vp, _f32, _vp, _vp]),
     "gdn_prefill_gated": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32,
                                     _i32, _f32, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _sz, _vp]),
+    "gdn_linear_prefill_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32]),
+    "gdn_linear_prefill": (C.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _i32,
+                                     _f32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "gdn_linear_prefill_backward_workspace_size": (_sz, [_i32, _i64, _i32, _i32, _i32]),
+    "gdn_linear_prefill_backward": (C.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _i64, _i32,
+                                              _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp,
+                                              _sz, _vp]),
+    "gdn_linear_decode_step": (C.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _i32,
+                                         _vp, _i32, _vp, _i32, _vp]),
+    "gdn_state_copy": (C.c_int, [_vp, _i32, _i32, _vp, _vp, _i32, _vp]),
+    "gdn_state_workspace_size": (_sz, [_i32]),
+    "gdn_state_fork": (C.c_int, [_vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "gdn_state_compact": (C.c_int, [_vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "gdn_state_free": (C.c_int, [_vp, _i32, _vp, _i32, _vp]),
 }
+
+
+class StateBuffer(C.Structure):
+    """gdn_state_buffer."""
+    _fields_ = [("data", C.c_void_p), ("slot_bytes", C.c_int64)]
+
+
 
 
 class GdnError(RuntimeError):
@@ -609,3 +630,276 @@ def _backward(entry, q, k, v, a, b, A_log, dt_bias, d_o, d_final_state, cu_seqle
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check(entry, st)
     return out
+
+
+class _Launch:
+    """The device and stream a call runs on: the device of its tensors (which must share one), made current for
+    the call, and `stream` or that device's current stream, which allocations of the call then belong to."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+        self.device = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("all tensors must be CUDA tensors")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError(f"all tensors must be on one device, got {self.device} and {t.device}")
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+        self.scopes = []
+        if self.device.index != torch.cuda.current_device():
+            self.scopes.append(torch.cuda.device(self.device))
+        if stream is not None:
+            self.scopes.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        import torch
+        for s in self.scopes:
+            s.__enter__()
+        return C.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *e):
+        for s in reversed(self.scopes):
+            s.__exit__(*e)
+
+
+def _token_rows(t, T, H, d, name):
+    """Checks a bf16 [T, H, d] tensor whose tokens may be any multiple of 8 elements apart (a view of a packed
+    projection); returns that distance, 0 for a dense tensor."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (T, H, d):
+        raise ValueError(f"{name}: expected shape {(T, H, d)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    s = t.stride()
+    if s[2] != 1 or (H > 1 and s[1] != d) or s[0] < H * d or s[0] % 8 != 0:
+        raise ValueError(f"{name}: heads must be contiguous and tokens a multiple of 8 elements apart, got strides {s}")
+    return s[0]
+
+
+def _linear_shapes(q, k, v, g, cu_seqlens):
+    import torch
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [T, heads, d]")
+    T, Hqk, d = q.shape
+    Hv = v.shape[1]
+    n_seq = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    lds = (_token_rows(q, T, Hqk, d, "q"), _token_rows(k, T, Hqk, d, "k"), _token_rows(v, T, Hv, d, "v"))
+    if g.dim() not in (1, 2):
+        raise ValueError(f"g: expected shape {(T, Hv)} or {(Hv,)}, got {tuple(g.shape)}")
+    _need(g, torch.float32, (T, Hv) if g.dim() == 2 else (Hv,), "g")
+    if cu_seqlens is not None:
+        _need(cu_seqlens, torch.int32, (n_seq + 1,), "cu_seqlens")
+    return T, Hqk, Hv, d, n_seq, lds
+
+
+def _given(t, dtype, shape, name, device):
+    """An output: the caller's, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _need(t, dtype, shape, name)
+
+
+def _workspace(workspace, size, device):
+    """(the caller's workspace or a new one, its bytes)"""
+    import torch
+    if workspace is None:
+        return torch.empty(size, dtype=torch.uint8, device=device), size
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def linear_prefill_workspace_size(n_seq, T, Hqk, Hv, d=128) -> int:
+    return int(lib().gdn_linear_prefill_workspace_size(n_seq, T, Hqk, Hv, d))
+
+
+def linear_prefill(q, k, v, g, cu_seqlens=None, scale=None, initial_state=None, final_state=None, o=None,
+                   workspace=None, want_final_state=True, stream=None, o_dtype=None):
+    """gdn_linear_prefill: linear attention with a decay per head, S_t = e^g S_{t-1} + v_t k_t^T, o_t = scale S_t q_t,
+    over packed sequences.  q, k [T, Hqk, d], v [T, Hv, d] bf16 (dense, or views of a packed projection), g float32
+    [T, Hv] or [Hv].  Returns (o [T, Hv, d] of o_dtype: bf16 by default, or float32; final_state [N, Hv, d, d] f32 or
+    None)."""
+    import torch
+    T, Hqk, Hv, d, n_seq, lds = _linear_shapes(q, k, v, g, cu_seqlens)
+    if o_dtype is None:
+        o_dtype = o.dtype if o is not None else torch.bfloat16
+    if o_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("o must be float32 or bfloat16")
+    if initial_state is not None:
+        _need(initial_state, torch.float32, (n_seq, Hv, d, d), "initial_state")
+    if scale is None:
+        scale = d ** -0.5
+    with _Launch(stream, q, k, v, g, cu_seqlens, initial_state, final_state, o, workspace) as s:
+        dev = q.device
+        o = _given(o, o_dtype, (T, Hv, d), "o", dev)
+        if final_state is not None or want_final_state:
+            final_state = _given(final_state, torch.float32, (n_seq, Hv, d, d), "final_state", dev)
+        ws, ws_bytes = _workspace(workspace, lib().gdn_linear_prefill_workspace_size(n_seq, T, Hqk, Hv, d), dev)
+        st = lib().gdn_linear_prefill(_ptr(q), _ptr(k), _ptr(v), *lds, _ptr(g), g.dim() - 1, _ptr(cu_seqlens), n_seq,
+                                      T, Hqk, Hv, d, float(scale), _ptr(initial_state), _ptr(final_state), _ptr(o),
+                                      int(o_dtype == torch.bfloat16), _ptr(ws), ws_bytes, s)
+    _check("gdn_linear_prefill", st)
+    return o, final_state
+
+
+def linear_prefill_backward(q, k, v, g, d_o, d_final_state=None, cu_seqlens=None, scale=None, initial_state=None,
+                            want_d_initial=True, workspace=None, stream=None, out=None, grad_dtype=None):
+    """gdn_linear_prefill_backward: gradients of a loss with dL/do = d_o [T, Hv, d] bf16 and dL/dS_T = d_final_state
+    [N, Hv, d, d] float32 (or zero).  Returns a dict of dq, dk [T, Hqk, d], dv [T, Hv, d] (grad_dtype: bf16 by
+    default, or float32), dg (float32, shaped as g) and d_initial_state [N, Hv, d, d] float32 (or None).  out: an
+    optional dict of preallocated tensors under those names."""
+    import torch
+    T, Hqk, Hv, d, n_seq, lds = _linear_shapes(q, k, v, g, cu_seqlens)
+    given = out or {}
+    if grad_dtype is None:
+        grad_dtype = next((given[n].dtype for n in ("dq", "dk", "dv") if given.get(n) is not None), torch.bfloat16)
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the gradients must be float32 or bfloat16")
+    _need(d_o, torch.bfloat16, (T, Hv, d), "d_o")
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        if t is not None:
+            _need(t, torch.float32, (n_seq, Hv, d, d), name)
+    if scale is None:
+        scale = d ** -0.5
+    with _Launch(stream, q, k, v, g, d_o, cu_seqlens, initial_state, d_final_state, workspace, *given.values()) as s:
+        dev = q.device
+        out = {n: _given(given.get(n), dt, shape, n, dev) for n, dt, shape in (
+            ("dq", grad_dtype, (T, Hqk, d)), ("dk", grad_dtype, (T, Hqk, d)), ("dv", grad_dtype, (T, Hv, d)),
+            ("dg", torch.float32, tuple(g.shape)))}
+        out["d_initial_state"] = _given(given.get("d_initial_state"), torch.float32, (n_seq, Hv, d, d),
+                                        "d_initial_state", dev) if want_d_initial else None
+        size = lib().gdn_linear_prefill_backward_workspace_size(n_seq, T, Hqk, Hv, d)
+        ws, ws_bytes = _workspace(workspace, size, dev)
+        st = lib().gdn_linear_prefill_backward(
+            _ptr(q), _ptr(k), _ptr(v), *lds, _ptr(g), g.dim() - 1, _ptr(cu_seqlens), n_seq, T, Hqk, Hv, d,
+            float(scale), _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
+            _ptr(out["dv"]), int(grad_dtype == torch.bfloat16), _ptr(out["dg"]), _ptr(out["d_initial_state"]),
+            _ptr(ws), ws_bytes, s)
+    _check("gdn_linear_prefill_backward", st)
+    return out
+
+
+def linear_decode_step(q, k, v, g, state, n_seq, layers, slot=None, scale=None, o=None, stream=None, o_dtype=None):
+    """gdn_linear_decode_step: one token of linear attention for n_seq sequences x `layers` layers.  q, k
+    [n_seq*layers, Hqk, d], v [n_seq*layers, Hv, d] bf16, g float32 [n_seq*layers, Hv] or [layers, Hv], state
+    [n_slots*layers, Hv, d, d] float32 or bf16, updated in place, slot [n_seq] int32 (-1: no sequence) or None.
+    Returns o [n_seq*layers, Hv, d] (o_dtype: float32 by default, or bf16)."""
+    import torch
+    U, Hqk, d = q.shape
+    Hv = v.shape[1]
+    if U != n_seq * layers or layers <= 0:
+        raise ValueError("q.shape[0] must equal n_seq * layers")
+    _need(q, torch.bfloat16, (U, Hqk, d), "q")
+    _need(k, torch.bfloat16, (U, Hqk, d), "k")
+    _need(v, torch.bfloat16, (U, Hv, d), "v")
+    per_unit = g.shape[0] != layers or n_seq == 1
+    _need(g, torch.float32, (U if per_unit else layers, Hv), "g")
+    n_slots = state.shape[0] // layers
+    bf16 = state.dtype == torch.bfloat16
+    _need(state, torch.bfloat16 if bf16 else torch.float32, (n_slots * layers, Hv, d, d), "state")
+    if slot is not None:
+        _need(slot, torch.int32, (n_seq,), "slot")
+    if o_dtype is None:
+        o_dtype = o.dtype if o is not None else torch.float32
+    if o_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("o must be float32 or bfloat16")
+    if scale is None:
+        scale = d ** -0.5
+    with _Launch(stream, q, k, v, g, state, slot, o) as s:
+        o = _given(o, o_dtype, (U, Hv, d), "o", q.device)
+        st = lib().gdn_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_unit), _ptr(slot), n_seq, layers,
+                                          Hqk, Hv, d, float(scale), n_slots, _ptr(state), int(bf16), _ptr(o),
+                                          int(o_dtype == torch.bfloat16), s)
+    _check("gdn_linear_decode_step", st)
+    return o
+
+
+def _state_buffers(buffers, n_slots=None):
+    """(gdn_state_buffer array, number of buffers, number of slots) of a cache's tensors [n_slots, ...]."""
+    import torch
+    if isinstance(buffers, torch.Tensor):
+        buffers = [buffers]
+    array = (StateBuffer * max(len(buffers), 1))()
+    for i, b in enumerate(buffers):
+        if b.dim() < 1 or not b.is_contiguous():
+            raise ValueError("a cache's buffers must be contiguous, [n_slots, ...]")
+        if n_slots is None:
+            n_slots = b.shape[0]
+        if b.shape[0] != n_slots:
+            raise ValueError(f"a cache's buffers must have one number of slots, got {b.shape[0]} and {n_slots}")
+        array[i].data = b.data_ptr()
+        array[i].slot_bytes = b.numel() // max(n_slots, 1) * b.element_size()
+    if n_slots is None:
+        raise ValueError("a cache has at least one buffer")
+    return array, len(buffers), n_slots, list(buffers)
+
+
+def _index(t, n, name):
+    import torch
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be one-dimensional")
+    return _need(t, torch.int32, (t.shape[0] if n is None else n,), name)
+
+
+def state_copy(buffers, src, dst, stream=None):
+    """gdn_state_copy: page[dst[i]] = page[src[i]] for all i at once (each source as it was before the call), a page
+    being one slot of every tensor [n_slots, ...] in `buffers`.  src, dst [n] int32; an index outside the cache makes
+    its entry void, and of several entries with one destination the last holds."""
+    array, nb, n_slots, tensors = _state_buffers(buffers)
+    _index(src, None, "src")
+    n = src.shape[0]
+    _index(dst, n, "dst")
+    with _Launch(stream, src, dst, *tensors) as s:
+        st = lib().gdn_state_copy(array, nb, n_slots, _ptr(src), _ptr(dst), n, s)
+    _check("gdn_state_copy", st)
+
+
+def _state_workspace(workspace, n_slots, device):
+    return _workspace(workspace, lib().gdn_state_workspace_size(n_slots), device)
+
+
+def state_fork(buffers, live, src, dst=None, workspace=None, stream=None):
+    """gdn_state_fork: new pages for `src` [n] int32, each filled from that live slot or, for -1, with zeros, in the
+    lowest free slots.  live [n_slots] int32 is updated.  Returns dst [n] int32 (-1 where none was free)."""
+    import torch
+    _index(live, None, "live")
+    array, nb, n_slots, tensors = _state_buffers(buffers, live.shape[0])
+    _index(src, None, "src")
+    n = src.shape[0]
+    with _Launch(stream, live, src, dst, workspace, *tensors) as s:
+        dst = _given(dst, torch.int32, (n,), "dst", live.device)
+        ws, ws_bytes = _state_workspace(workspace, n_slots, live.device)
+        st = lib().gdn_state_fork(array, nb, n_slots, _ptr(live), _ptr(src), _ptr(dst), n, _ptr(ws), ws_bytes, s)
+    _check("gdn_state_fork", st)
+    return dst
+
+
+def state_compact(buffers, live, moved=None, workspace=None, stream=None):
+    """gdn_state_compact: moves the live pages into the first slots with the fewest moves.  live [n_slots] int32 is
+    updated.  Returns moved [n_slots] int32, the new slot of each page (-1: free)."""
+    import torch
+    _index(live, None, "live")
+    array, nb, n_slots, tensors = _state_buffers(buffers, live.shape[0])
+    with _Launch(stream, live, moved, workspace, *tensors) as s:
+        moved = _given(moved, torch.int32, (n_slots,), "moved", live.device)
+        ws, ws_bytes = _state_workspace(workspace, n_slots, live.device)
+        st = lib().gdn_state_compact(array, nb, n_slots, _ptr(live), _ptr(moved), _ptr(ws), ws_bytes, s)
+    _check("gdn_state_compact", st)
+    return moved
+
+
+def state_free(live, slots, stream=None):
+    """gdn_state_free: live[slots[i]] = 0 (indices outside the cache are ignored); the pages keep their contents."""
+    _index(live, None, "live")
+    _index(slots, None, "slots")
+    with _Launch(stream, live, slots) as s:
+        st = lib().gdn_state_free(_ptr(live), live.shape[0], _ptr(slots), slots.shape[0], s)
+    _check("gdn_state_free", st)

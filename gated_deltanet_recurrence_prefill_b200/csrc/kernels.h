@@ -154,6 +154,94 @@ size_t prefill_pc_workspace_bytes(int32_t n_seq, int32_t Hv);
 // workspace the single-CTA kernel needs (and the least gdn_prefill accepts)
 size_t prefill_min_workspace_bytes(int32_t n_seq, int32_t Hv);
 
+// linear attention with a decay per head (gdn_linear_*)
+struct LinearArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t ldq, ldk, ldv;         // elements from a token to the next
+    const float* g;
+    int64_t ldg;                   // Hv: a log decay per (token, head); 0: one per head
+    const int32_t* cu_seqlens;     // NULL: one sequence of length T
+    int32_t n_seq;
+    int64_t T;
+    int32_t Hqk;
+    int32_t Hv;
+    float scale;
+    const float* initial_state;    // may be NULL
+    float* final_state;            // may be NULL
+    void* o;
+    int32_t o_bf16;
+    void* workspace;
+};
+size_t linear_prefill_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hv);
+cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t stream);
+
+struct LinearBackwardArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t ldq, ldk, ldv;
+    const float* g;
+    int64_t ldg;
+    const int32_t* cu_seqlens;
+    int32_t n_seq;
+    int64_t T;
+    int32_t Hqk;
+    int32_t Hv;
+    float scale;
+    const float* initial_state;    // may be NULL
+    const uint16_t* d_o;
+    const float* d_final_state;    // may be NULL
+    void* dq;
+    void* dk;
+    void* dv;
+    int32_t grad_bf16;
+    float* dg;
+    float* d_initial_state;        // may be NULL
+    void* workspace;
+};
+size_t linear_backward_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv);
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t stream);
+
+// one token of it for n_seq x layers units (linear_decode.cu)
+struct LinearDecodeArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const float* g;
+    int32_t g_per_unit;            // 0: [layers, Hv]
+    const int32_t* slot;           // NULL: slot n for sequence n
+    int32_t n_seq;
+    int32_t layers;
+    int32_t Hqk;
+    int32_t Hv;
+    float scale;
+    int32_t n_slots;
+    void* state;
+    int32_t state_bf16;
+    void* o;
+    int32_t o_bf16;
+};
+cudaError_t launch_linear_decode(const LinearDecodeArgs& a, cudaStream_t stream);
+
+// pages of a state cache (state_pool.cu)
+constexpr int kMaxStateBuffers = 8;
+struct StateBuffers {
+    uint8_t* data[kMaxStateBuffers];
+    int64_t bytes[kMaxStateBuffers];       // of a slot
+    int32_t n;
+    int32_t n_slots;
+};
+size_t state_workspace_bytes(int32_t n_slots);
+cudaError_t launch_state_copy(const StateBuffers& b, const int32_t* src, const int32_t* dst, int32_t n,
+                              cudaStream_t stream);
+cudaError_t launch_state_fork(const StateBuffers& b, int32_t* live, const int32_t* src, int32_t* dst, int32_t n,
+                              void* workspace, cudaStream_t stream);
+cudaError_t launch_state_compact(const StateBuffers& b, int32_t* live, int32_t* moved, void* workspace,
+                                 cudaStream_t stream);
+cudaError_t launch_state_free(int32_t* live, int32_t n_slots, const int32_t* slots, int32_t n, cudaStream_t stream);
+
 // workspace layout shared by the prefill kernels
 constexpr size_t kWsErrorWordOffset = 0;     // uint32 error word (0 = ok)
 constexpr size_t kWsHeaderBytes = 256;

@@ -603,6 +603,158 @@ gdn_status gdn_selftest_bounded_wait(int32_t which, int64_t limit_us, void* work
 gdn_status gdn_gated_norm(const float* o, const uint16_t* z, const float* norm_w, int64_t T, int32_t Hv,
                           int32_t d, int32_t layers, float eps, uint16_t* y, gdn_stream_t stream);
 
+/*
+ * ---- Linear attention with a decay for each head ---------------------------
+ *
+ * The recurrence without the delta rule's erasing term: per value head, with a
+ * log decay g (<= 0),
+ *     S_t = e^{g_t} S_{t-1} + v_t k_t^T,      o_t = scale * S_t q_t.
+ * Shapes, head sharing, packed sequences and the state's layout are those of
+ * gdn_prefill and gdn_decode_step (d = 128, value head h reads key head
+ * h / (Hv / Hqk), state [.., Hv, d_v, d_k] float32), so the front end, the gated
+ * norm and the state cache serve these layers too.
+ *
+ * Common to the three entry points:
+ *  q, k, v   bf16; token t of head h starts at q + t * ldq + h * d (elements), so
+ *            that views of one packed projection need no copy.  ld = 0 stands for
+ *            the dense H * d; otherwise a multiple of 8, at least H * d.
+ *  g         float32, [T, Hv] (g_per_token = 1) or [Hv] (g_per_token = 0: fixed
+ *            decays).  A log decay below -104, -inf included, is taken as -104,
+ *            whose decay is 0 in float32: the state is reset.  NaN stays NaN.
+ *  cu_seqlens[n_seq] may be less than T here: the tokens behind the last sequence
+ *            are not read and their outputs are left as they were.
+ */
+
+/*
+ * gdn_linear_prefill_workspace_size -- bytes of device workspace for
+ * gdn_linear_prefill (a multiple of 256, never 0): a header whose first word is
+ * the error word that gdn_prefill_status and gdn_check_async read, and the states
+ * at the joints of sequences that are worked on in several parts.  Host-only.
+ */
+size_t gdn_linear_prefill_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, int32_t d);
+
+/*
+ * gdn_linear_prefill -- the recurrence over packed sequences.
+ *  initial_state  [n_seq, Hv, d_v, d_k] float32 or NULL (zeros).
+ *  final_state    the same shape or NULL (not written); may be initial_state.  A
+ *                 sequence of length 0 hands its initial state on.
+ *  o              [T, Hv, d], float32 (o_bf16 = 0) or bf16 (o_bf16 = 1).
+ *  workspace      gdn_linear_prefill_workspace_size() bytes, 256-byte aligned;
+ *                 calls that share it must be ordered on one stream.
+ * The final state is exact to float32 rounding; o carries the rounding to bf16 of
+ * the score matrix and of the state that the tokens meet (relative 2^-8 each).
+ * Errors as for gdn_prefill.
+ */
+gdn_status gdn_linear_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t ldq, int64_t ldk,
+                              int64_t ldv, const float* g, int32_t g_per_token, const int32_t* cu_seqlens,
+                              int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, int32_t d, float scale,
+                              const float* initial_state, float* final_state, void* o, int32_t o_bf16,
+                              void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* Bytes of device workspace for gdn_linear_prefill_backward (a multiple of 256, never 0).  Host-only. */
+size_t gdn_linear_prefill_backward_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, int32_t d);
+
+/*
+ * gdn_linear_prefill_backward -- the gradient of a scalar loss through
+ * gdn_linear_prefill, given dL/do and dL/dS_T.
+ *  d_o            [T, Hv, d] bf16.
+ *  d_final_state  [n_seq, Hv, d_v, d_k] float32 or NULL (zero).
+ * Outputs (overwritten):
+ *  dq, dk         [T, Hqk, d] (summed in float32 over the value heads of each key
+ *                 head) and dv [T, Hv, d], all float32 (grad_bf16 = 0) or bf16 (1).
+ *  dg             float32, shaped as g ([Hv]: summed over all tokens).
+ *  d_initial_state [n_seq, Hv, d_v, d_k] float32 or NULL (not written); may not be
+ *                 d_final_state.
+ * No atomics: the result is deterministic.  dg and d_initial_state are exact to
+ * float32 rounding; dq, dk and dv as o in the prefill.  A log decay at or below
+ * -104 has gradient 0.
+ */
+gdn_status gdn_linear_prefill_backward(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t ldq,
+                                       int64_t ldk, int64_t ldv, const float* g, int32_t g_per_token,
+                                       const int32_t* cu_seqlens, int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv,
+                                       int32_t d, float scale, const float* initial_state, const uint16_t* d_o,
+                                       const float* d_final_state, void* dq, void* dk, void* dv, int32_t grad_bf16,
+                                       float* dg, float* d_initial_state, void* workspace, size_t workspace_bytes,
+                                       gdn_stream_t stream);
+
+/*
+ * gdn_linear_decode_step -- one token of the recurrence for n_seq sequences x
+ * `layers` layers, unit u = sequence * layers + layer, state updated in place.
+ *  q, k    [U, Hqk, d] bf16 (dense), v [U, Hv, d] bf16, U = n_seq * layers.
+ *  g       float32, [U, Hv] (g_per_unit = 1) or [layers, Hv] (g_per_unit = 0).
+ *  slot    [n_seq] int32 (device): the slot of each sequence's states, or NULL for
+ *          slot n (then n_slots >= n_seq).  A slot outside [0, n_slots), such as
+ *          -1, marks a row of the batch without a sequence: no state is touched
+ *          and its outputs are 0.  The others must be distinct.
+ *  state   [n_slots, layers, Hv, d_v, d_k], float32 (state_bf16 = 0) or bf16 (1:
+ *          rounded to nearest even when stored, the arithmetic is float32).
+ *  o       [U, Hv, d], float32 (o_bf16 = 0) or bf16 (1), from the updated state
+ *          before it is rounded.
+ */
+gdn_status gdn_linear_decode_step(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* g,
+                                  int32_t g_per_unit, const int32_t* slot, int32_t n_seq, int32_t layers, int32_t Hqk,
+                                  int32_t Hv, int32_t d, float scale, int32_t n_slots, void* state,
+                                  int32_t state_bf16, void* o, int32_t o_bf16, gdn_stream_t stream);
+
+/*
+ * ---- Pages of a state cache -------------------------------------------------
+ *
+ * A page is one slot of every buffer of a cache: of the recurrent states and the
+ * convolution histories that gdn_decode_step_fused and gdn_linear_decode_step
+ * address by `slot`, or of any array whose leading axis is the slot.  The buffers
+ * are given by a host array (read during the call):
+ */
+typedef struct gdn_state_buffer {
+    void* data;            /* device, 16-byte aligned: [n_slots, ...], dense */
+    int64_t slot_bytes;    /* bytes of one slot, a positive multiple of 16 */
+} gdn_state_buffer;
+
+/* At most this many buffers per call (GDN_ERR_UNSUPPORTED above), and this many entries in a copy. */
+#define GDN_MAX_STATE_BUFFERS 8
+#define GDN_MAX_STATE_COPIES 1024
+
+/*
+ * gdn_state_copy -- page[dst[i]] = page[src[i]] for all i at once: every entry
+ * reads its source as it was before the call, so reorderings in place (the beams
+ * of a search), swaps and copies of one page to many are all one call.
+ *  src, dst  [n] int32 (device), n <= GDN_MAX_STATE_COPIES.  Entries with an index
+ *            outside [0, n_slots) are ignored; of several entries with one
+ *            destination the last holds.
+ * Each page is read and written once; no workspace.
+ */
+gdn_status gdn_state_copy(const gdn_state_buffer* buffers, int32_t n_buffers, int32_t n_slots, const int32_t* src,
+                          const int32_t* dst, int32_t n, gdn_stream_t stream);
+
+/* Bytes of device workspace for gdn_state_fork and gdn_state_compact.  Host-only. */
+size_t gdn_state_workspace_size(int32_t n_slots);
+
+/*
+ * gdn_state_fork -- new pages: entry i takes a free slot, written to dst[i], which
+ * is filled from page src[i], or with zeros where src[i] = -1, and marked live.
+ *  live  [n_slots] int32 (device), nonzero for the slots in use; updated.
+ *  src   [n] int32: -1 or a live slot.  Any other entry takes none (dst[i] = -1).
+ *  dst   [n] int32 output.  Free slots are given out in rising order, to the
+ *        entries in order; where they run out, dst[i] = -1.
+ *  workspace  gdn_state_workspace_size() bytes, 16-byte aligned.
+ */
+gdn_status gdn_state_fork(const gdn_state_buffer* buffers, int32_t n_buffers, int32_t n_slots, int32_t* live,
+                          const int32_t* src, int32_t* dst, int32_t n, void* workspace, size_t workspace_bytes,
+                          gdn_stream_t stream);
+
+/*
+ * gdn_state_compact -- moves the live pages into the slots [0, n_live), with as
+ * few moves as that takes: the live slots from n_live on fill the free ones before
+ * it, both in rising order; the others stay.
+ *  live   [n_slots] int32, as for gdn_state_fork; afterwards 1 for the first n_live
+ *         slots and 0 for the rest.
+ *  moved  [n_slots] int32 output: the new slot of each page, -1 for a free slot.
+ */
+gdn_status gdn_state_compact(const gdn_state_buffer* buffers, int32_t n_buffers, int32_t n_slots, int32_t* live,
+                             int32_t* moved, void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* gdn_state_free -- live[slots[i]] = 0; indices outside [0, n_slots) are ignored.  The pages keep their contents. */
+gdn_status gdn_state_free(int32_t* live, int32_t n_slots, const int32_t* slots, int32_t n, gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
