@@ -1,0 +1,377 @@
+// linear_walk.cu -- launches of the linear attention passes (linear_walk.cuh):
+// the prefill is one pass, its gradients are three (linear_attn.h).
+#include <cuda.h>
+
+#include "linear_walk.cuh"
+
+namespace gdn {
+
+namespace {
+
+using namespace lin;
+
+constexpr int kSms = 148;
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// ---- parts --------------------------------------------------------------------------------------------
+// The length of a part, from what the host knows (T tokens in n_seq sequences, of which it assumes equal
+// lengths): the least of
+//     walk:  rounds of `heads` CTAs per part over the SMs, each reps * chunks * kWalk + kStart long
+//     states, where a sequence has several parts:  the same over all parts but the last, chunks * kState,
+//            and the scan
+// in microseconds, measured on B200.  Sequences that turn out longer than a part are cut.
+int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, int64_t most) {
+    constexpr double kWalk = 0.9, kStateStep = 0.5, kStart = 5.0, kScan = 6.0;
+    const int64_t chunks = (T + n_seq - 1) / n_seq / kC + 1;
+    double best = 0.0;
+    int64_t len = chunks;
+    for (int64_t parts = 1; parts <= chunks && parts <= kSms; ++parts) {
+        const int64_t l = (chunks + parts - 1) / parts;
+        if (l * kC > most) continue;
+        const int64_t n = (chunks + l - 1) / l;
+        auto rounds = [&](int64_t ctas) { return (double)((ctas + kSms - 1) / kSms); };
+        double cost = rounds((int64_t)n_seq * n * heads) * ((double)(l * reps) * kWalk + kStart);
+        if (n > 1)
+            cost += rounds((int64_t)n_seq * (n - 1) * heads * reps) * ((double)l * kStateStep + kStart) + kScan;
+        if (best == 0.0 || cost < best) {
+            best = cost;
+            len = n == 1 && n_seq > 1 ? 2 * l : l;         // uneven sequences: up to twice the mean stay whole
+        }
+    }
+    if (len * kC > most) len = most / kC;
+    return (int32_t)(len * kC);
+}
+
+int32_t part_count(int32_t n_seq, int64_t T, int32_t part_len) { return (int32_t)(T / part_len) + n_seq; }
+
+// Turns each part's own sum into its starting state: start' = decay * start + own along the parts of a
+// sequence, in the pass's direction, from init.  One CTA per (sequence, head, 1024 elements).
+constexpr int kScanThreads = 256;
+
+__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_constant__ Walk w) {
+    __shared__ int32_t before_sm[kScanThreads / 32];
+    const int seq = blockIdx.x / w.p.Hv, h = blockIdx.x % w.p.Hv;
+    auto parts = [&](int i) {
+        const int64_t a = w.p.cu ? w.p.cu[i] : 0, b = w.p.cu ? w.p.cu[i + 1] : w.p.T;
+        return b > a ? (int32_t)((b - a + w.part_len - 1) / w.part_len) : 1;
+    };
+    const int n = parts(seq);
+    if (n == 1) return;
+    int32_t before = 0;
+    for (int i = threadIdx.x; i < seq; i += kScanThreads) before += parts(i);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) before += __shfl_xor_sync(0xffffffffu, before, m);
+    if ((threadIdx.x & 31) == 0) before_sm[threadIdx.x >> 5] = before;
+    __syncthreads();
+    before = 0;
+    for (int i = 0; i < kScanThreads / 32; ++i) before += before_sm[i];
+    const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
+    auto slot = [&](int k) { return (int64_t)(before + (w.p.backward ? n - 1 - k : k)) * w.p.Hv + h; };
+    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (w.p.init) run = *reinterpret_cast<const float4*>(w.p.init + ((int64_t)seq * w.p.Hv + h) * (kD * kD) + e);
+    constexpr int kBatch = 4;                   // parts whose sums are in flight at once
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+        float4 own[kBatch];
+        float decay[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (k0 + k < n - 1) {
+                own[k] = *reinterpret_cast<const float4*>(w.joint + slot(k0 + k) * (kD * kD) + e);
+                decay[k] = w.joint_decay[slot(k0 + k)];
+            }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (k0 + k < n) {
+                *reinterpret_cast<float4*>(w.joint + slot(k0 + k) * (kD * kD) + e) = run;
+                if (k0 + k < n - 1) {
+                    run.x = fmaf(decay[k], run.x, own[k].x);
+                    run.y = fmaf(decay[k], run.y, own[k].y);
+                    run.z = fmaf(decay[k], run.z, own[k].z);
+                    run.w = fmaf(decay[k], run.w, own[k].w);
+                }
+            }
+    }
+}
+
+// The decays' gradient (linear_attn.h's passes give r_t = q_t . dq_t and c_t = k_t . dk_t): with S and dS the
+// state and its gradient behind token t,
+//     dg_t = <S_end, dS_end> + sum_{t' >= t, same part} (r_t' - c_t'),
+// the first term at the part's end from the joints (or the final state), the sums in 64 bits from the last
+// token back.  One CTA per (part, head).
+constexpr int kDgThreads = 256;
+
+GDN_DEVICE double block_sum(double x, double* sm) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < kDgThreads / 32; ++i) s += sm[i];
+    __syncthreads();
+    return s;
+}
+
+__global__ void __launch_bounds__(kDgThreads)
+lin_dg_kernel(const __grid_constant__ Walk w, const float* r, const float* c, const float* joint_end, const float* fin,
+              const float* d_fin, float* dg, double* part_sum) {
+    __shared__ double sm[kDgThreads / 32];
+    const int Hv = w.p.Hv;
+    const int32_t index = blockIdx.x / Hv;
+    const int h = blockIdx.x % Hv, tid = threadIdx.x;
+    const Part part = find_part(w, index);
+    if (part.seq < 0) {
+        if (part_sum && tid == 0) part_sum[(int64_t)index * Hv + h] = 0.0;
+        return;
+    }
+    const float *a = nullptr, *b = nullptr;
+    if (!part.last) {
+        a = w.joint + ((int64_t)(index + 1) * Hv + h) * (kD * kD);
+        b = joint_end + ((int64_t)index * Hv + h) * (kD * kD);
+    } else if (d_fin) {
+        a = fin + ((int64_t)part.seq * Hv + h) * (kD * kD);
+        b = d_fin + ((int64_t)part.seq * Hv + h) * (kD * kD);
+    }
+    double behind = 0.0;
+    if (a) {
+        for (int i = tid * 4; i < kD * kD; i += kDgThreads * 4) {
+            const float4 x = *reinterpret_cast<const float4*>(a + i), y = *reinterpret_cast<const float4*>(b + i);
+            behind += ((double)x.x * y.x + (double)x.y * y.y) + ((double)x.z * y.z + (double)x.w * y.w);
+        }
+        behind = block_sum(behind, sm);
+    }
+    double total = 0.0;
+    for (int64_t end = part.t1; end > part.t0; end -= kDgThreads) {
+        // thread 0 takes the last token of the block
+        const int64_t t = end - 1 - tid;
+        const bool there = t >= part.t0;
+        double x = there ? (double)r[(int64_t)h * w.p.T + t] - (double)c[(int64_t)h * w.p.T + t] : 0.0;
+        double upto = x;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, upto, m);
+            if ((tid & 31) >= m) upto += y;
+        }
+        if ((tid & 31) == 31) sm[tid >> 5] = upto;
+        __syncthreads();
+        double all = 0.0;
+        for (int i = 0; i < kDgThreads / 32; ++i) {
+            if (i < (tid >> 5)) upto += sm[i];
+            all += sm[i];
+        }
+        __syncthreads();
+        if (there) {
+            const double d = w.p.g[t * w.p.ldg + h] <= kLinMinLogDecay ? 0.0 : behind + upto;
+            if (!part_sum) dg[t * Hv + h] = (float)d;
+            total += d;
+        }
+        behind += all;
+    }
+    if (part_sum) {
+        total = block_sum(total, sm);
+        if (tid == 0) part_sum[(int64_t)index * Hv + h] = total;
+    }
+}
+
+// dg of decays that all tokens share: the parts' sums, one warp per head
+__global__ void lin_dg_sum_kernel(const double* part_sum, int32_t n_parts, int32_t Hv, float* dg) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    double s = 0.0;
+    for (int i = lane; i < n_parts; i += 32) s += part_sum[(int64_t)i * Hv + h];
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lane == 0) dg[h] = (float)s;
+}
+
+// ---- launches -------------------------------------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// looked up once per process; null if the driver does not provide it
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &found) == cudaSuccess &&
+            found == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(ptr);
+        cudaGetLastError();    // a refused query leaves no sticky error behind
+        return nullptr;
+    }();
+    return fn;
+}
+
+// rows of an operand as 64 x 64 boxes, 128-byte swizzle
+bool make_map(CUtensorMap* m, const LinOperand& o, int64_t T, int32_t Hv) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)(Hv / o.rep) * kD, (cuuint64_t)T};
+    cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
+    cuuint32_t box[2] = {64, 64};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(o.p), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kMode>
+cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
+    CUtensorMap mx{}, my{}, mz{}, mu{};
+    if (!make_map(&my, w.p.y, w.p.T, w.p.Hv) || !make_map(&mz, w.p.z, w.p.T, w.p.Hv) ||
+        (kMode != kState && !make_map(&mx, w.p.x, w.p.T, w.p.Hv)) ||
+        (kMode == kExact && !make_map(&mu, w.p.u, w.p.T, w.p.Hv)))
+        return cudaErrorInvalidValue;
+    const int64_t blocks = (int64_t)w.n_parts * (kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(lin_walk_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Layout<kMode>::kAlloc);
+    if (e != cudaSuccess) return e;
+    lin_walk_kernel<kMode><<<(unsigned)blocks, kThreads, Layout<kMode>::kAlloc, s>>>(mx, my, mz, mu, w);
+    return cudaGetLastError();
+}
+
+// the starting states of all parts: each part's own sum, then the scan
+cudaError_t launch_joints(const Walk& w, cudaStream_t s) {
+    cudaError_t e = launch_walk<kState>(w, s);
+    if (e != cudaSuccess) return e;
+    lin_scan_kernel<<<dim3((unsigned)(w.p.n_seq * w.p.Hv), kD * kD / (kScanThreads * 4)), kScanThreads, 0, s>>>(w);
+    return cudaGetLastError();
+}
+
+// no tokens at all: the states pass through
+cudaError_t pass_state(const float* from, float* to, int32_t n_seq, int32_t Hv, cudaStream_t s) {
+    if (!to || to == from) return cudaSuccess;
+    const size_t bytes = (size_t)n_seq * Hv * kD * kD * 4;
+    return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, bytes, s);
+}
+
+struct Joints {
+    int32_t part_len, n_parts, split;
+    size_t state_bytes, decay_bytes;
+};
+
+Joints plan_joints(int32_t n_seq, int64_t T, int32_t Hv, int32_t heads, int64_t most) {
+    Joints j;
+    j.part_len = choose_part_len(n_seq, T, heads, Hv / heads, most);
+    j.n_parts = part_count(n_seq, T, j.part_len);
+    j.split = T > j.part_len;
+    if (!j.split) j.n_parts = n_seq;
+    j.state_bytes = j.split ? up256((size_t)j.n_parts * Hv * kD * kD * 4) : 0;
+    j.decay_bytes = j.split ? up256((size_t)j.n_parts * Hv * 4) : 0;
+    return j;
+}
+
+constexpr int64_t kAnyLength = (int64_t)1 << 30;
+
+struct BackwardPlan {
+    Joints j;
+    size_t qdq, kdk, acc, fin, sums, fwd, bwd, decay_f, decay_b, bytes;
+};
+
+BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
+    BackwardPlan b;
+    // parts of at most 4096 tokens: the decays' gradient is a running sum along a part
+    b.j = plan_joints(n_seq, T, Hv, Hqk, 4096);
+    size_t off = kWsHeaderBytes;
+    auto take = [&](size_t bytes) { const size_t at = off; off += up256(bytes); return at; };
+    b.qdq = take((size_t)T * Hv * 4);
+    b.kdk = take((size_t)T * Hv * 4);
+    b.acc = take(Hv > Hqk ? (size_t)T * Hqk * kD * 4 : 0);
+    b.fin = take((size_t)n_seq * Hv * kD * kD * 4);
+    b.sums = take((size_t)b.j.n_parts * Hv * 8);
+    b.fwd = take(b.j.state_bytes);
+    b.bwd = take(b.j.state_bytes);
+    b.decay_f = take(b.j.decay_bytes);
+    b.decay_b = take(b.j.decay_bytes);
+    b.bytes = off;
+    return b;
+}
+
+}  // namespace
+
+size_t linear_prefill_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hv) {
+    const Joints j = plan_joints(n_seq, T, Hv, Hv, kAnyLength);
+    return kWsHeaderBytes + j.state_bytes + j.decay_bytes;
+}
+
+cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
+    char* ws = static_cast<char*>(a.workspace);
+    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
+    if (e != cudaSuccess) return e;
+    if (a.T == 0) return pass_state(a.initial_state, a.final_state, a.n_seq, a.Hv, s);
+    const Joints j = plan_joints(a.n_seq, a.T, a.Hv, a.Hv, kAnyLength);
+    Walk w{};
+    w.part_len = j.part_len; w.n_parts = j.n_parts; w.split = j.split;
+    w.joint = reinterpret_cast<float*>(ws + kWsHeaderBytes);
+    w.joint_decay = reinterpret_cast<float*>(ws + kWsHeaderBytes + j.state_bytes);
+    w.err = reinterpret_cast<uint32_t*>(ws + kWsErrorWordOffset);
+    LinPass& p = w.p;
+    p.x = {a.q, a.ldq, a.Hv / a.Hqk};
+    p.y = {a.k, a.ldk, a.Hv / a.Hqk};
+    p.z = {a.v, a.ldv, 1};
+    p.g = a.g; p.ldg = a.ldg; p.cu = a.cu_seqlens; p.n_seq = a.n_seq; p.T = a.T; p.Hv = a.Hv; p.scale = a.scale;
+    p.init = a.initial_state; p.fin = a.final_state;
+    p.out = a.o; p.out_bf16 = a.o_bf16;
+    if (j.split && (e = launch_joints(w, s)) != cudaSuccess) return e;
+    return launch_walk<kOut>(w, s);
+}
+
+size_t linear_backward_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
+    return backward_plan(n_seq, T, Hqk, Hv).bytes;
+}
+
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) {
+    const BackwardPlan b = backward_plan(a.n_seq, a.T, a.Hqk, a.Hv);
+    char* ws = static_cast<char*>(a.workspace);
+    auto floats = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
+    if (e != cudaSuccess) return e;
+    if (a.T == 0) {
+        e = pass_state(a.d_final_state, a.d_initial_state, a.n_seq, a.Hv, s);
+        return e == cudaSuccess && !a.ldg ? cudaMemsetAsync(a.dg, 0, (size_t)a.Hv * 4, s) : e;
+    }
+    const int rep = a.Hv / a.Hqk;
+    const LinOperand q{a.q, a.ldq, rep}, k{a.k, a.ldk, rep}, v{a.v, a.ldv, 1}, d_o{a.d_o, (int64_t)a.Hv * kD, 1};
+    Walk base{};
+    base.part_len = b.j.part_len; base.n_parts = b.j.n_parts; base.split = b.j.split;
+    base.err = reinterpret_cast<uint32_t*>(ws + kWsErrorWordOffset);
+    base.p.g = a.g; base.p.ldg = a.ldg; base.p.cu = a.cu_seqlens; base.p.n_seq = a.n_seq; base.p.T = a.T;
+    base.p.Hv = a.Hv; base.p.scale = a.scale; base.p.out_bf16 = a.grad_bf16;
+    Walk fwd = base, bwd = base;
+    fwd.joint = floats(b.fwd); fwd.joint_decay = floats(b.decay_f);
+    bwd.joint = floats(b.bwd); bwd.joint_decay = floats(b.decay_b);
+    bwd.p.backward = 1;
+    if (b.j.split) {                            // S at the parts' starts, dS at their ends
+        Walk w = fwd;
+        w.p.y = k; w.p.z = v; w.p.init = a.initial_state;
+        if ((e = launch_joints(w, s)) != cudaSuccess) return e;
+        w = bwd;
+        w.p.y = q; w.p.z = d_o; w.p.init = a.d_final_state;
+        if ((e = launch_joints(w, s)) != cudaSuccess) return e;
+    }
+    float* fin = a.d_final_state ? floats(b.fin) : nullptr;
+    Walk w = fwd;                               // dq: its state is S^T
+    w.p.x = d_o; w.p.y = v; w.p.z = k; w.p.u = q; w.p.dots = floats(b.qdq);
+    w.p.init = a.initial_state; w.p.fin = fin; w.p.state_t = 1; w.joint_t = 1;
+    w.p.out = a.dq; w.p.out_rep = rep; w.p.acc = floats(b.acc);
+    if ((e = launch_walk<kExact>(w, s)) != cudaSuccess) return e;
+    w = bwd;                                    // dk: dS^T
+    w.p.x = v; w.p.y = d_o; w.p.z = q; w.p.u = k; w.p.dots = floats(b.kdk);
+    w.p.init = a.d_final_state; w.p.state_t = 1; w.joint_t = 1;
+    w.p.out = a.dk; w.p.out_rep = rep; w.p.acc = floats(b.acc);
+    if ((e = launch_walk<kExact>(w, s)) != cudaSuccess) return e;
+    w = bwd;                                    // dv: dS
+    w.p.x = k; w.p.y = q; w.p.z = d_o;
+    w.p.init = a.d_final_state; w.p.fin = a.d_initial_state;
+    w.p.out = a.dv;
+    if ((e = launch_walk<kOut>(w, s)) != cudaSuccess) return e;
+    double* sums = a.ldg ? nullptr : reinterpret_cast<double*>(ws + b.sums);
+    lin_dg_kernel<<<(unsigned)(b.j.n_parts * a.Hv), kDgThreads, 0, s>>>(fwd, floats(b.qdq), floats(b.kdk), bwd.joint, fin,
+                                                                    a.d_final_state, a.dg, sums);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.ldg) return e;
+    lin_dg_sum_kernel<<<a.Hv, 32, 0, s>>>(sums, b.j.n_parts, a.Hv, a.dg);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn
