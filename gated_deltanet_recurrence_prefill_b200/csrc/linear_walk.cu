@@ -183,6 +183,17 @@ __global__ void lin_dg_sum_kernel(const double* part_sum, int32_t n_parts, int32
     if (lane == 0) dg[h] = (float)s;
 }
 
+// acc [tokens, width] in float32 -> out in bf16, for the tokens that sequences own; 8 elements a thread
+__global__ void __launch_bounds__(256) lin_round_kernel(const float* acc, uint16_t* out, const int32_t* cu, int32_t n_seq,
+                                                        int64_t T, int32_t width) {
+    const int64_t n = (cu ? (int64_t)cu[n_seq] : T) * (width / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const float4 a = reinterpret_cast<const float4*>(acc)[2 * i], b = reinterpret_cast<const float4*>(acc)[2 * i + 1];
+        reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
+                                                      pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    }
+}
+
 // ---- launches -------------------------------------------------------------------------------------------
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -215,11 +226,27 @@ bool make_map(CUtensorMap* m, const LinOperand& o, int64_t T, int32_t Hv) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the output's rows as 32-row boxes of 128 bytes, 128-byte swizzle
+bool make_out_map(CUtensorMap* m, const LinPass& p) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const bool f32 = p.out_rep > 1 || !p.out_bf16;
+    void* base = f32 && p.out_bf16 ? p.acc : p.out;
+    const cuuint64_t width = (cuuint64_t)(p.Hv / p.out_rep) * kD;
+    cuuint64_t dims[2] = {width, (cuuint64_t)p.T};
+    cuuint64_t strides[1] = {width * (f32 ? 4 : 2)};
+    cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kMode>
 cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
-    CUtensorMap mx{}, my{}, mz{}, mu{};
+    CUtensorMap mx{}, my{}, mz{}, mu{}, mo{};
     if (!make_map(&my, w.p.y, w.p.T, w.p.Hv) || !make_map(&mz, w.p.z, w.p.T, w.p.Hv) ||
-        (kMode != kState && !make_map(&mx, w.p.x, w.p.T, w.p.Hv)) ||
+        (kMode != kState && (!make_map(&mx, w.p.x, w.p.T, w.p.Hv) || !make_out_map(&mo, w.p))) ||
         (kMode == kExact && !make_map(&mu, w.p.u, w.p.T, w.p.Hv)))
         return cudaErrorInvalidValue;
     const int64_t blocks = (int64_t)w.n_parts * (kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep);
@@ -227,8 +254,16 @@ cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(lin_walk_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Layout<kMode>::kAlloc);
     if (e != cudaSuccess) return e;
-    lin_walk_kernel<kMode><<<(unsigned)blocks, kThreads, Layout<kMode>::kAlloc, s>>>(mx, my, mz, mu, w);
-    return cudaGetLastError();
+    lin_walk_kernel<kMode><<<(unsigned)blocks, kThreads, Layout<kMode>::kAlloc, s>>>(mx, my, mz, mu, mo, w);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (kMode != kState && w.p.out_rep > 1 && w.p.out_bf16) {
+        const int32_t width = w.p.Hv / w.p.out_rep * kD;
+        const int64_t n = (w.p.T * (width / 8) + 255) / 256;
+        lin_round_kernel<<<(unsigned)(n < kSms * 8 ? n : kSms * 8), 256, 0, s>>>(
+            w.p.acc, static_cast<uint16_t*>(w.p.out), w.p.cu, w.p.n_seq, w.p.T, width);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 // the starting states of all parts: each part's own sum, then the scan

@@ -29,14 +29,26 @@
 // at once.  One CTA per (part, output head); the value heads that share an
 // output row are taken in turn by one CTA, which adds them in float32.
 //
-// Roles in a CTA of 16 warps, handing over through mbarriers (every wait is
-// bounded; one that gives up raises the workspace's error word):
-//   warps 0-7    the state in registers (64 columns a thread), its bf16 copy,
-//                and the output: the chunk's inter and intra
-//   warps 8-11   w z in three parts, one z index a thread
-//   warps 12-13  the scores, one token a thread
-//   warp  14     TMA loads and the chunk's decays
-//   warp  15     issues the products
+// Roles in a CTA of 28 warps, handing over through mbarriers:
+//   warps 0-7    the state in registers (64 columns a thread), its bf16 copy
+//   warps 8-15   the output: the chunk's inter and intra
+//   warps 16-19  w z in three parts (kState: the even slots)
+//   warps 20-23  the scores         (kState: w z, the odd slots)
+//   warp  24     TMA loads
+//   warp  25     issues KV's products
+//   warp  26     issues the others
+//   warp  27     the chunk's decays; it waits for every stage to come round, and for
+//                the other roles to end, at most two seconds each, and makes every
+//                other wait give up when that is over (the error word is raised)
+// What bounds it is issue slots (2,200 instructions a chunk and scheduler) and the
+// hand-overs between the roles, so:
+//  - w z and u are read, and the output is written, as transposed 8 x 8 matrices
+//    (ldmatrix / stmatrix), whose fragments are those of TMEM's 16-lane shapes; with
+//    two-byte accesses the shared-memory pipe took 16 cycles each (7,300 cycles a chunk);
+//  - the output leaves by TMA, and float32 pairs go through two-wide instructions;
+//  - x is loaded twice, one copy below the other, so that the scores' product has
+//    every row in two TMEM quadrants and four warps share them;
+//  - two threads issue products: one of them alone was busy throughout (4,400 cycles).
 #pragma once
 
 #include <cuda.h>
@@ -55,7 +67,7 @@ enum Mode { kOut = 0, kExact = 1, kState = 2 };
 
 constexpr int kD = 128;
 constexpr int kC = 64;                          // tokens of a chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 896;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kPanel = 64 * 128;           // 64 rows of 64 bf16, 128-byte swizzle
 constexpr uint32_t kTile = 2 * kPanel;          // 64 rows of 128
@@ -124,29 +136,37 @@ GDN_DEVICE Part find_part(const Walk& w, int32_t index) {
     return r;
 }
 
+// registers of the warpgroups: launched with 72 each
+constexpr int kRegsState = 104, kRegsOut = 56, kRegsScores = 56, kRegsRest = 56;
+static_assert(2 * kRegsState + 2 * kRegsOut + 72 + kRegsScores + kRegsRest <= 7 * 72, "the launch's registers");
+
 template <int kMode>
 struct Layout {
     static constexpr bool kOuts = kMode != kState;
     static constexpr int kParts = kMode == kExact ? 3 : 1;         // of A and of the scores
-    // shared memory: stages of [x] y z [u] tiles, the scores, decays per stage, barriers
-    static constexpr uint32_t kX = 0;
-    static constexpr uint32_t kY = kOuts ? kTile : 0;
+    // shared memory: stages of [x twice] y z [u] tiles, the scores, decays per stage, barriers
+    static constexpr uint32_t kX = 0;                              // per panel: 64 rows, and the same again
+    static constexpr uint32_t kY = kOuts ? 2 * kTile : 0;
     static constexpr uint32_t kZ = kY + kTile;
     static constexpr uint32_t kU = kZ + kTile;
     static constexpr uint32_t kStage = kU + (kMode == kExact ? kTile : 0);
-    static constexpr int kStages = kMode == kExact ? 3 : kMode == kOut ? 4 : 6;
+    static constexpr int kStages = kMode == kExact ? 2 : kMode == kOut ? 3 : 6;
+    // a chunk's output before it leaves, over x and y: per half of its tokens panels of 32 rows of 128 bytes
+    // (64 bf16 or 32 float32), 128-byte swizzle
+    static constexpr uint32_t kRows = 32 * 128, kHalf = 4 * kRows;
+    static_assert(!kOuts || 2 * kHalf <= kZ, "the output's rows");
     static constexpr uint32_t kScores = kStages * kStage;
     static constexpr uint32_t kGates = kScores + (kOuts ? kParts * kPanel : 0);
     // a stage's decays: a[64], w[64], exponent high and low [64] each, gamma, tokens
     static constexpr uint32_t kGateBytes = (4 * 64 + 4) * 4;
-    static constexpr uint32_t kDots = kGates + kStages * kGateBytes;       // [8 warps][32] partial dot products
-    static constexpr uint32_t kBars = kDots + (kMode == kExact ? 8 * 32 * 4 : 0);
+    static constexpr uint32_t kDots = kGates + kStages * kGateBytes;       // [2][8 warps][32] partial dot products
+    static constexpr uint32_t kBars = kDots + (kMode == kExact ? 2 * 8 * 32 * 4 : 0);
     // barriers
     static constexpr int bFull = 0, bEmpty = bFull + kStages, bPFull = bEmpty + kStages, bPReady = bPFull + 1,
                          bAReady = bPReady + 1, bKvFull = bAReady + 1, bKvFree = bKvFull + 1, bOFull = bKvFree + 1,
                          bOFree = bOFull + 1, bWFull = bOFree + 1, bWFree = bWFull + 2, bZeroed = bWFree + 2,
-                         bDots = bZeroed + 1, bDrain = bDots + 2, kBarCount = bDrain + 1;
-    static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag, part
+                         bRows = bZeroed + 1, bDrain = bRows + 2, bDone = bDrain + 2, kBarCount = bDone + 1;
+    static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag
     static constexpr uint32_t kSmem = kMisc + 64;
     static constexpr uint32_t kAlloc = kSmem + 1024;
     static_assert(kAlloc <= 232448, "a CTA's shared memory");
@@ -161,14 +181,42 @@ struct Layout {
 static_assert(Layout<kExact>::tW + 2 * Layout<kExact>::kSlotCols <= 512 && Layout<kOut>::tW + 2 * Layout<kOut>::kSlotCols <= 512,
               "TMEM columns");
 
+// pairs of float32 operations in one instruction
+GDN_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+GDN_DEVICE float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+GDN_DEVICE float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+GDN_DEVICE float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
+
 // x = hi + mid + lo in bf16 for a pair of values: 8 bits each, cut, so that the remainders are exact
-GDN_DEVICE void split3(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
-    const float r0 = x0 - __uint_as_float(b0 & 0xffff0000u), r1 = x1 - __uint_as_float(b1 & 0xffff0000u);
-    const uint32_t m0 = __float_as_uint(r0), m1 = __float_as_uint(r1);
+GDN_DEVICE void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint32_t b0 = __float_as_uint(x.x), b1 = __float_as_uint(x.y);
+    const float2 r = sub2(x, make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)));
+    const uint32_t m0 = __float_as_uint(r.x), m1 = __float_as_uint(r.y);
+    const float2 l = sub2(r, make_float2(__uint_as_float(m0 & 0xffff0000u), __uint_as_float(m1 & 0xffff0000u)));
     hi = __byte_perm(b0, b1, 0x7632);
     mid = __byte_perm(m0, m1, 0x7632);
-    lo = pack_bf16x2(r0 - __uint_as_float(m0 & 0xffff0000u), r1 - __uint_as_float(m1 & 0xffff0000u));
+    lo = pack_bf16x2(l.x, l.y);
 }
 
 // ex2.approx keeps 2^-22 relative; exponents here are <= 0
@@ -178,6 +226,19 @@ GDN_DEVICE float exp2_fast(float x) {
     return r;
 }
 
+// the stages in turn: index and parity of its uses
+template <int kStages>
+struct Ring {
+    int st = 0;
+    uint32_t phase = 0;
+    GDN_DEVICE void next() {
+        if (++st == kStages) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 // everything a role needs
 struct Ctx {
     const Walk& w;
@@ -185,15 +246,17 @@ struct Ctx {
     uint32_t base;                  // its shared-space address
     uint32_t tmem;
     volatile int* abort;
+    uint32_t abort_at;              // its shared-space address
     Part part;
-    int32_t chunks;                 // of the part
+    int32_t index;                  // of the part
+    int32_t chunks;                 // of it
     int32_t head;                   // output head (kState: value head)
     int32_t reps;                   // value heads to take in turn
     int32_t head0;                  // the first of them
 
     GDN_DEVICE uint32_t bar(uint32_t bars, int i) const { return base + bars + i * 8; }
     GDN_DEVICE bool wait(uint32_t bars, int i, uint32_t parity) const {
-        return mbar_wait(bar(bars, i), parity & 1u, abort, kWaitLimitNs);
+        return mbar_wait_watched(bar(bars, i), parity & 1u, abort_at);
     }
     // first token of the n-th chunk in the pass's direction
     GDN_DEVICE int64_t chunk_start(int32_t n) const {
@@ -201,285 +264,402 @@ struct Ctx {
     }
 };
 
-// ---- warp 14: loads and decays ------------------------------------------------------------------------
+GDN_DEVICE void commit_to(const Ctx& c, uint32_t bars, int i) { mma_commit(c.bar(bars, i)); }
+
+// ---- warp 24: loads ----------------------------------------------------------------------------------
 template <int kMode>
 GDN_DEVICE void load_role(const Ctx& c, const CUtensorMap* mx, const CUtensorMap* my, const CUtensorMap* mz,
                           const CUtensorMap* mu) {
     using L = Layout<kMode>;
-    const int lane = threadIdx.x & 31;
+    if ((threadIdx.x & 31) != 0) return;
     const LinPass& p = c.w.p;
-    const int32_t total = c.reps * c.chunks;
-    int32_t issued = 0;
-    for (int32_t it = 0; it < total; ++it) {
-        const int st = it % L::kStages;
-        const int32_t n = it % c.chunks, h = c.head0 + it / c.chunks;
-        if (it >= L::kStages && !c.wait(L::kBars, L::bEmpty + st, it / L::kStages - 1)) break;
-        const int64_t t = c.chunk_start(n);
-        const int valid = (int)min((int64_t)kC, c.part.t1 - t);
-        const uint32_t full = c.bar(L::kBars, L::bFull + st);
-        if (lane == 0) {
-            const uint32_t s = c.base + st * L::kStage;
+    Ring<L::kStages> ring;
+    int32_t it = 0;
+    for (int r = 0; r < c.reps; ++r) {
+        const int h = c.head0 + r;
+        const int32_t x0 = h / p.x.rep * kD, y0 = h / p.y.rep * kD, z0 = h / p.z.rep * kD;
+        const int32_t u0 = kMode == kExact ? h / p.u.rep * kD : 0;
+        int32_t t = (int32_t)c.chunk_start(0);
+        const int32_t step = p.backward ? -kC : kC;
+#pragma unroll 1
+        for (int32_t n = 0; n < c.chunks; ++n, ++it, t += step, ring.next()) {
+            if (it >= L::kStages && !c.wait(L::kBars, L::bEmpty + ring.st, ring.phase ^ 1u)) goto out;
+            const uint32_t full = c.bar(L::kBars, L::bFull + ring.st), s = c.base + ring.st * L::kStage;
             mbar_arrive_expect_tx(full, L::kStage);
+#pragma unroll 1
             for (int k = 0; k < 2; ++k) {
-                if (L::kOuts) tma_load_2d(s + L::kX + k * kPanel, mx, h / p.x.rep * kD + k * 64, (int32_t)t, full);
-                tma_load_2d(s + L::kY + k * kPanel, my, h / p.y.rep * kD + k * 64, (int32_t)t, full);
-                tma_load_2d(s + L::kZ + k * kPanel, mz, h / p.z.rep * kD + k * 64, (int32_t)t, full);
-                if (kMode == kExact) tma_load_2d(s + L::kU + k * kPanel, mu, h / p.u.rep * kD + k * 64, (int32_t)t, full);
+                tma_load_2d(s + L::kY + k * kPanel, my, y0 + k * 64, t, full);
+                if (L::kOuts) {
+                    tma_load_2d(s + L::kX + k * kTile, mx, x0 + k * 64, t, full);
+                    tma_load_2d(s + L::kX + k * kTile + kPanel, mx, x0 + k * 64, t, full);
+                }
+                tma_load_2d(s + L::kZ + k * kPanel, mz, z0 + k * 64, t, full);
+                if (kMode == kExact) tma_load_2d(s + L::kU + k * kPanel, mu, u0 + k * 64, t, full);
             }
         }
-        issued = it + 1;
-        // the sums of log decays (base 2) in 64 bits: two tokens a lane
-        const int i0 = 2 * lane, i1 = i0 + 1;
-        float g0 = i0 < valid ? p.g[(t + i0) * p.ldg + h] : 0.f;
-        float g1 = i1 < valid ? p.g[(t + i1) * p.ldg + h] : 0.f;
-        g0 = g0 < kLinMinLogDecay ? kLinMinLogDecay : g0;
-        g1 = g1 < kLinMinLogDecay ? kLinMinLogDecay : g1;
-        const double kLog2e = 1.4426950408889634;
-        const double d0 = (double)g0 * kLog2e, d1 = (double)g1 * kLog2e;
-        double upto = d0 + d1;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, upto, m);
-            if (lane >= m) upto += x;
-        }
-        const double all = __shfl_sync(0xffffffffu, upto, 31);
-        const double G0 = upto - d1, G1 = upto;
-        float* gate = reinterpret_cast<float*>(c.sm + L::kGates + st * L::kGateBytes);
-        const float e0 = exp2f((float)G0), e1 = exp2f((float)G1);                // from the chunk's start
-        const float f0 = exp2f((float)(all - G0)), f1 = exp2f((float)(all - G1));    // to its end
-        const bool bw = p.backward != 0;
-        const float ws = bw ? p.scale : 1.f;
-        reinterpret_cast<float2*>(gate)[lane] = make_float2(bw ? f0 : e0, bw ? f1 : e1);
-        reinterpret_cast<float2*>(gate + 64)[lane] = make_float2(i0 < valid ? ws * (bw ? e0 : f0) : 0.f,
-                                                                 i1 < valid ? ws * (bw ? e1 : f1) : 0.f);
-        // the exponent of Gamma_ts is E_t - E_s; as high (a multiple of 2^-10, so that differences of the
-        // high parts are exact: |E| < 64 * 151) and low part
-        const double E0 = bw ? -G0 : G0, E1 = bw ? -G1 : G1;
-        const double h0 = rint(E0 * 1024.0) * (1.0 / 1024.0), h1 = rint(E1 * 1024.0) * (1.0 / 1024.0);
-        reinterpret_cast<float2*>(gate + 128)[lane] = make_float2((float)h0, (float)h1);
-        reinterpret_cast<float2*>(gate + 192)[lane] = make_float2((float)(E0 - h0), (float)(E1 - h1));
-        if (lane == 0) {
-            gate[256] = exp2f((float)all);
-            reinterpret_cast<int32_t*>(gate)[257] = valid;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
     }
-    // loads still in flight land before the CTA may exit
+out:
+    // loads still in flight land before the CTA may exit: the last use of each stage
     volatile int no_abort = 0;
-    for (int32_t it = issued > L::kStages ? issued - L::kStages : 0; it < issued; ++it)
-        mbar_wait(c.bar(L::kBars, L::bFull + it % L::kStages), (it / L::kStages) & 1, &no_abort, kWaitLimitNs);
+#pragma unroll 1
+    for (int k = 0; k < L::kStages && it > 0; ++k) {
+        if (ring.st == 0) ring.phase ^= 1u;
+        ring.st = ring.st == 0 ? L::kStages - 1 : ring.st - 1;
+        --it;
+        mbar_wait(c.bar(L::kBars, L::bFull + ring.st), ring.phase, &no_abort, kWaitLimitNs);
+    }
 }
 
-// ---- warp 15: products ---------------------------------------------------------------------------------
+// ---- warp 27: decays -----------------------------------------------------------------------------------
+// Sums of log decays to base 2 in fixed point, 2^-32 a step (64 tokens of at most 151 fit 46 bits): exact sums
+// and differences, one integer add a step.
 template <int kMode>
-GDN_DEVICE void mma_role(const Ctx& c) {
+GDN_DEVICE void decay_role(const Ctx& c) {
+    using L = Layout<kMode>;
+    const int lane = threadIdx.x & 31;
+    const LinPass& p = c.w.p;
+    const bool bw = p.backward != 0;
+    const float ws = bw ? p.scale : 1.f;
+    const int i0 = 2 * lane, i1 = i0 + 1;                       // this lane's tokens
+    auto fixed = [](float g) {
+        // exp of what is beyond these limits is 0 or inf in float32
+        g = g < kLinMinLogDecay ? kLinMinLogDecay : g > -kLinMinLogDecay ? -kLinMinLogDecay : g;
+        return __double2ll_rn((double)g * (1.4426950408889634 * 4294967296.0));
+    };
+    auto high = [](long long x) { return (float)(int)(x >> 22) * (1.f / 1024.f); };             // a multiple of 2^-10
+    auto low = [](long long x) { return (float)(int)(x & 0x3fffff) * (1.f / 4294967296.f); };   // the rest, >= 0
+    Ring<L::kStages> ring;
+    int32_t it = 0;
+    for (int r = 0; r < c.reps; ++r) {
+        // this lane's log decays of a chunk, fetched a chunk ahead
+        const int64_t step = (int64_t)(bw ? -kC : kC);
+        int64_t t = c.chunk_start(0);
+        const float* g = p.g + c.head0 + r + (t + i0) * p.ldg;
+        float n0 = t + i0 < c.part.t1 && c.chunks > 0 ? g[0] : 0.f, n1 = t + i1 < c.part.t1 && c.chunks > 0 ? g[p.ldg] : 0.f;
+#pragma unroll 1
+        for (int32_t n = 0; n < c.chunks; ++n, ++it, ring.next()) {
+            const float g0 = n0, g1 = n1;
+            const int valid = (int)min((int64_t)kC, c.part.t1 - t);
+            t += step;
+            g += step * p.ldg;
+            n0 = n + 1 < c.chunks && t + i0 < c.part.t1 ? g[0] : 0.f;
+            n1 = n + 1 < c.chunks && t + i1 < c.part.t1 ? g[p.ldg] : 0.f;
+            // a NaN reaches every sum that has its token
+            const unsigned nan0 = __ballot_sync(0xffffffffu, g0 != g0), nan1 = __ballot_sync(0xffffffffu, g1 != g1);
+            const unsigned earlier = (1u << lane) - 1u;
+            const long long d1 = fixed(g1);
+            long long G1 = fixed(g0) + d1;
+#pragma unroll 1
+            for (int m = 1; m < 32; m <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, G1, m);
+                if (lane >= m) G1 += x;
+            }
+            const long long G0 = G1 - d1, all = __shfl_sync(0xffffffffu, G1, 31);
+            const float bad = (nan0 | nan1) ? __int_as_float(0x7fc00000) : 0.f;          // added where a NaN counts
+            const float bad0 = (((nan0 | nan1) & earlier) | (nan0 & (1u << lane))) ? bad : 0.f;
+            const float bad1 = (bad0 != bad0 || (nan1 & (1u << lane))) ? bad : 0.f;
+            const float e0 = exp2_fast(high(G0) + low(G0) + bad0), e1 = exp2_fast(high(G1) + low(G1) + bad1);
+            const float f0 = exp2_fast(high(all - G0) + low(all - G0) + bad), f1 = exp2_fast(high(all - G1) + low(all - G1) + bad);
+            // (the bound of all waits of the CTA: a stage comes round within kWaitLimitNs)
+            if (it >= L::kStages &&
+                !mbar_wait(c.bar(L::kBars, L::bEmpty + ring.st), ring.phase ^ 1u, c.abort, kWaitLimitNs))
+                return;
+            float* gate = reinterpret_cast<float*>(c.sm + L::kGates + ring.st * L::kGateBytes);
+            reinterpret_cast<float2*>(gate)[lane] = make_float2(bw ? f0 : e0, bw ? f1 : e1);
+            reinterpret_cast<float2*>(gate + 64)[lane] = make_float2(i0 < valid ? ws * (bw ? e0 : f0) : 0.f,
+                                                                     i1 < valid ? ws * (bw ? e1 : f1) : 0.f);
+            // the exponent of Gamma_ts is E_t - E_s; kExact: high parts (whose differences are exact) and low ones
+            const float sg = bw ? -1.f : 1.f;
+            const float l0 = kMode == kExact ? 0.f : low(G0), l1 = kMode == kExact ? 0.f : low(G1);
+            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * (high(G0) + l0) + bad0, sg * (high(G1) + l1) + bad1);
+            if (kMode == kExact) reinterpret_cast<float2*>(gate + 192)[lane] = make_float2(sg * low(G0), sg * low(G1));
+            if (lane == 31) {
+                gate[256] = e1;                                 // the whole chunk's decay
+                reinterpret_cast<int32_t*>(gate)[257] = valid;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bFull + ring.st));
+        }
+    }
+}
+
+// ---- warps 25 and 26: products ---------------------------------------------------------------------------
+// (Unrolled: in rolled loops an issue took up to 200 cycles, more than any of these products.)
+template <int kMode>
+GDN_DEVICE uint64_t k_major(const Ctx& c, int st, uint32_t tile) {
+    return sdesc_sw128(c.base + st * Layout<kMode>::kStage + tile, 16, 1024);
+}
+template <int kMode>
+GDN_DEVICE uint64_t mn_major(const Ctx& c, int st, uint32_t tile) {
+    return sdesc_sw128(c.base + st * Layout<kMode>::kStage + tile, kPanel, 1024);
+}
+
+// products still in flight end before TMEM is freed
+GDN_DEVICE void drain(const Ctx& c, uint32_t bar) {
+    volatile int no_abort = 0;
+    mma_commit(bar);
+    mbar_wait(bar, 0, &no_abort, kWaitLimitNs);
+}
+
+// KV = (w z)^T y, slot by slot
+template <int kMode>
+GDN_DEVICE void kv_role(const Ctx& c) {
     using L = Layout<kMode>;
     if ((threadIdx.x & 31) != 0) return;
     constexpr uint32_t idKv = idesc_bf16(128, 128, false, true);
+    const int32_t total = c.reps * c.chunks;
+    Ring<L::kStages> ring;
+    uint32_t odd = 0;                           // parity of the chunk, and of the uses of the barriers once a chunk
+    bool ok = true;
+#pragma unroll 1
+    for (int32_t it = 0; it < total; ++it, ring.next(), odd ^= 1u) {
+        if (!c.wait(L::kBars, L::bFull + ring.st, ring.phase)) break;
+        // the accumulator has been read for the chunk before
+        if (it > 0 && !c.wait(L::kBars, L::bKvFree, odd ^ 1u)) break;
+        const uint64_t dy = mn_major<kMode>(c, ring.st, L::kY);
+#pragma unroll
+        for (int s = 0; s < L::kSlots; ++s) {
+            // use number it * kSlots / 2 + s / 2 of the slot's barriers
+            ok = c.wait(L::kBars, L::bWFull + (s & 1), L::kSlots == 2 ? odd : (uint32_t)(s >> 1));
+            if (!ok) break;
+            tc_fence_after();
+            // smallest part first: the accumulator's rounding is then that of the largest part alone
+#pragma unroll
+            for (int part = 2; part >= 0; --part)
+#pragma unroll
+                for (int kk = 0; kk < L::kSlot / 16; ++kk)
+                    mma_bf16_ta(c.tmem + L::tKv,
+                                c.tmem + L::tW + (s & 1) * L::kSlotCols + part * (L::kSlot / 2) + kk * 8,
+                                dy + (s * (L::kSlot / 16) + kk) * 128, idKv, s > 0 || part < 2 || kk > 0);
+            commit_to(c, L::kBars, L::bWFree + (s & 1));
+        }
+        if (!ok) break;
+        commit_to(c, L::kBars, L::bKvFull);
+        commit_to(c, L::kBars, L::bEmpty + ring.st);
+    }
+    drain(c, c.bar(L::kBars, L::bDrain));
+}
+
+// inter = A x^T, intra = z^T scores^T, and P = x y^T of the chunk after (kExact: of the chunk itself, since intra
+// takes P's columns)
+template <int kMode>
+GDN_DEVICE void out_products_role(const Ctx& c) {
+    using L = Layout<kMode>;
+    if ((threadIdx.x & 31) != 0) return;
     constexpr uint32_t idKK = idesc_bf16(128, 64, false, false);
     constexpr uint32_t idPv = idesc_bf16(128, 64, true, false);
     const int32_t total = c.reps * c.chunks;
     const uint64_t dScores = sdesc_sw128(c.base + L::kScores, 16, 1024);
-    auto k_major = [&](int st, uint32_t tile) { return sdesc_sw128(c.base + st * L::kStage + tile, 16, 1024); };
-    auto mn_major = [&](int st, uint32_t tile) { return sdesc_sw128(c.base + st * L::kStage + tile, kPanel, 1024); };
-    auto k_step = [](int kk) { return (uint64_t)(((kk >> 2) * kPanel + (kk & 3) * 32) >> 4); };
-    auto commit = [&](int b) { mma_commit(c.bar(L::kBars, b)); };
-    // P = x y^T of chunk it
-    auto scores = [&](int32_t it) {
-        const int st = it % L::kStages;
-        const uint64_t dx = k_major(st, L::kX), dy = k_major(st, L::kY);
-        for (int kk = 0; kk < 8; ++kk) mma_bf16(c.tmem + L::tP, dx + k_step(kk), dy + k_step(kk), idKK, kk > 0);
-        commit(L::bPFull);
+    auto scores = [&](int st) {
+        const uint64_t dx = k_major<kMode>(c, st, L::kX), dy = k_major<kMode>(c, st, L::kY);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+            mma_bf16(c.tmem + L::tP, dx + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4),
+                     dy + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), idKK, kk > 0);
+        commit_to(c, L::kBars, L::bPFull);
     };
-    bool ok = true;
-    if (kMode == kOut && total > 0) {
-        ok = c.wait(L::kBars, L::bFull, 0);
-        tc_fence_after();
-        if (ok) scores(0);
-    }
-    for (int32_t it = 0; ok && it < total; ++it) {
-        const int st = it % L::kStages;
-        if (!c.wait(L::kBars, L::bFull + st, it / L::kStages)) break;
-        // KV = (w z)^T y, slot by slot; its accumulator has been read for the chunk before
-        const uint64_t dy = mn_major(st, L::kY);
-        for (int s = 0; ok && s < L::kSlots; ++s) {
-            const int32_t i = it * L::kSlots + s;
-            ok = c.wait(L::kBars, L::bWFull + (i & 1), i >> 1);
-            if (ok && s == 0 && it > 0) ok = c.wait(L::kBars, L::bKvFree, it - 1);
-            if (!ok) break;
+    Ring<L::kStages> ring;
+    uint32_t odd = 0;
+    // kOut: the extra first turn issues chunk 0's scores
+#pragma unroll 1
+    for (int32_t it = kMode == kOut ? -1 : 0; it < total; ++it) {
+        if (it >= 0) {
+            const int st = ring.st;
+            if (kMode == kExact && !c.wait(L::kBars, L::bFull + st, ring.phase)) break;
+            // inter and intra have been read for the chunk before
+            if (it > 0 && !c.wait(L::kBars, L::bOFree, odd ^ 1u)) break;
+            if (kMode == kExact) {
+                tc_fence_after();
+                scores(st);
+            }
+            if (!c.wait(L::kBars, L::bAReady, odd)) break;
             tc_fence_after();
-            const uint32_t a = c.tmem + L::tW + (i & 1) * L::kSlotCols;
-            // smallest part first: the accumulator's rounding is then that of the largest part alone
-            for (int part = 2; part >= 0; --part)
-                for (int kk = 0; kk < L::kSlot / 16; ++kk)
-                    mma_bf16_ta(c.tmem + L::tKv, a + part * (L::kSlot / 2) + kk * 8,
-                                dy + (s * (L::kSlot / 16) + kk) * 128, idKv, s > 0 || part < 2 || kk > 0);
-            commit(L::bWFree + (i & 1));
-        }
-        if (!ok) break;
-        commit(L::bKvFull);
-        if (kMode == kState) {
-            commit(L::bEmpty + st);
-            continue;
-        }
-        // inter and intra have been read for the chunk before
-        if (it > 0 && !c.wait(L::kBars, L::bOFree, it - 1)) break;
-        if (kMode == kExact) {
+            const uint64_t dx = k_major<kMode>(c, st, L::kX);
+#pragma unroll
+            for (int part = L::kParts - 1; part >= 0; --part)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ta(c.tmem + L::tInter, c.tmem + L::tA + part * 64 + kk * 8,
+                                dx + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4), idKK, part < L::kParts - 1 || kk > 0);
+            if (!c.wait(L::kBars, L::bPReady, odd)) break;
             tc_fence_after();
-            scores(it);
+            const uint64_t dz = mn_major<kMode>(c, st, L::kZ);
+#pragma unroll
+            for (int part = L::kParts - 1; part >= 0; --part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16(c.tmem + L::tIntra, dz + kk * 128, dScores + part * (kPanel >> 4) + kk * 2, idPv,
+                             part < L::kParts - 1 || kk > 0);
+            commit_to(c, L::kBars, L::bOFull);
+            commit_to(c, L::kBars, L::bEmpty + st);
+            ring.next();
+            odd ^= 1u;
         }
-        if (!c.wait(L::kBars, L::bAReady, it)) break;
-        tc_fence_after();
-        const uint64_t dx = k_major(st, L::kX);
-        for (int part = L::kParts - 1; part >= 0; --part)
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ta(c.tmem + L::tInter, c.tmem + L::tA + part * 64 + kk * 8, dx + k_step(kk), idKK,
-                            part < L::kParts - 1 || kk > 0);
-        if (!c.wait(L::kBars, L::bPReady, it)) break;
         if (kMode == kOut && it + 1 < total) {
-            if (!c.wait(L::kBars, L::bFull + (it + 1) % L::kStages, (it + 1) / L::kStages)) break;
+            if (!c.wait(L::kBars, L::bFull + ring.st, ring.phase)) break;
             tc_fence_after();
-            scores(it + 1);
+            scores(ring.st);
         }
-        tc_fence_after();
-        const uint64_t dz = mn_major(st, L::kZ);
-        for (int part = L::kParts - 1; part >= 0; --part)
-            for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(c.tmem + L::tIntra, dz + kk * 128, dScores + part * (kPanel >> 4) + kk * 2, idPv,
-                         part < L::kParts - 1 || kk > 0);
-        commit(L::bOFull);
-        commit(L::bEmpty + st);
     }
-    // products still in flight end before TMEM is freed
-    volatile int no_abort = 0;
-    commit(L::bDrain);
-    mbar_wait(c.bar(L::kBars, L::bDrain), 0, &no_abort, kWaitLimitNs);
+    drain(c, c.bar(L::kBars, L::bDrain + 1));
 }
 
-// ---- warps 8-11: w z in three parts ---------------------------------------------------------------------
+// rows valid .. 63 of a tile, by the 128 threads of a warpgroup
+GDN_DEVICE void clear_rows(uint8_t* tile, int valid) {
+#pragma unroll 1
+    for (int i = threadIdx.x & 127; i < (kC - valid) * 16; i += 128)
+        *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * kPanel + (valid + (i >> 4)) * 128 + (i & 7) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---- warps 16-19 (kState: 16-23): w z in three parts ------------------------------------------------------
+// One warpgroup takes all slots (first = 0, stride = 1), or two take every other one.
 template <int kMode>
-GDN_DEVICE void weight_role(const Ctx& c) {
+GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
     using L = Layout<kMode>;
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
-    const int z = quad * 32 + lane;                            // this thread's z index
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const int32_t total = c.reps * c.chunks;
-    uint32_t zeroed = 0;
-    // element (s, z) of a tile: panel z >> 6, row s, 16-byte piece (z & 63) >> 3 swizzled by s & 7
-    uint32_t at[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-        at[r] = (z >> 6) * kPanel + sw128_off(r, (z & 63) >> 3) + (z & 7) * 2;
-    for (int32_t it = 0; it < total; ++it) {
-        const int st = it % L::kStages;
-        if (!c.wait(L::kBars, L::bFull + st, it / L::kStages)) return;
-        uint8_t* stage = c.sm + st * L::kStage;
+    uint32_t zeroed = 0, odd = 0;
+    Ring<L::kStages> ring;
+    // This warp's z indices 32 quad .. + 32 as four 8 x 8 matrices (8 tokens each way) per ldmatrix: matrix m of
+    // 16 tokens is tokens 8 (m >> 1), z indices 8 (m & 1) (+ 16 for the second half); lane l gives row l % 8 of
+    // matrix l / 8.  Rows are 128 bytes, 16-byte pieces swizzled by the row.
+    const int row = ((lane >> 4) << 3) + (lane & 7);            // token of 16
+    const int z = quad * 32 + ((lane >> 3) & 1) * 8;
+    const uint32_t at = L::kZ + (z >> 6) * kPanel + sw128_off(row, (z & 63) >> 3);
+    const uint32_t at2 = L::kZ + (z >> 6) * kPanel + sw128_off(row, ((z + 16) & 63) >> 3);
+#pragma unroll 1
+    for (int32_t it = 0; it < total; ++it, ring.next(), odd ^= 1u) {
+        const int st = ring.st;
+        if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
         const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
         const int valid = reinterpret_cast<const int32_t*>(gate)[257];
         if (valid < kC) {
             // rows of y and z behind the part's last token belong to others and may hold anything: their
             // weights and scores are 0, and 0 times a NaN is not
-            for (int i = threadIdx.x & 127; i < (kC - valid) * 32; i += 128) {
-                const int row = valid + (i >> 5), piece = i & 31;
-                uint8_t* tile = stage + (piece & 16 ? L::kZ : L::kY) + ((piece >> 3) & 1) * kPanel;
-                *reinterpret_cast<uint4*>(tile + row * 128 + (piece & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
+            clear_rows(c.sm + st * L::kStage + L::kY, valid);
+            clear_rows(c.sm + st * L::kStage + L::kZ, valid);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bZeroed));
             if (!c.wait(L::kBars, L::bZeroed, zeroed++)) return;
         }
-        const uint8_t* tile = stage + L::kZ;
-        for (int s = 0; s < L::kSlots; ++s) {
-            const int32_t i = it * L::kSlots + s;
-            if (i >= 2 && !c.wait(L::kBars, L::bWFree + (i & 1), (i >> 1) - 1)) return;
+        const uint32_t tile = c.base + st * L::kStage;
+        // 16 tokens x 16 z indices at a time, the next matrices requested before these are worked on
+        uint32_t v[4], next[4];
+        ldmatrix_x4_trans(tile + at + first * L::kSlot * 128, next);
+#pragma unroll 1
+        for (int s = first; s < L::kSlots; s += stride) {
+            // (a barrier's phase before its first completes at once)
+            if (!c.wait(L::kBars, L::bWFree + (s & 1), (L::kSlots == 2 ? odd : (uint32_t)(s >> 1)) ^ 1u)) return;
             tc_fence_after();
-            const uint32_t dst = c.tmem + lanes + L::tW + (i & 1) * L::kSlotCols;
+            const uint32_t dst = c.tmem + lanes + L::tW + (s & 1) * L::kSlotCols;
+#pragma unroll 1
+            for (int t = s * L::kSlot; t < (s + 1) * L::kSlot; t += 16) {
+                // tokens t + 8 j + 2 (lane % 4) and the next
+                const float2 w0 = *reinterpret_cast<const float2*>(gate + 64 + t + 2 * (lane & 3));
+                const float2 w1 = *reinterpret_cast<const float2*>(gate + 64 + t + 8 + 2 * (lane & 3));
 #pragma unroll
-            for (int kk = 0; kk < L::kSlot / 16; ++kk) {
-                uint32_t part[3][8];
+                for (int hz = 0; hz < 2; ++hz) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = s * L::kSlot + kk * 16 + 2 * j;
-                    const float2 w = *reinterpret_cast<const float2*>(gate + 64 + t);
-                    const float z0 = bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + at[(2 * j) & 7] + (t >> 3) * 1024));
-                    const float z1 = bf16_to_f32(*reinterpret_cast<const uint16_t*>(tile + at[(2 * j + 1) & 7] + (t >> 3) * 1024));
-                    split3(w.x * z0, w.y * z1, part[0][j], part[1][j], part[2][j]);
+                    for (int m = 0; m < 4; ++m) v[m] = next[m];
+                    // (after a slot's last tokens the next slot's, which its first ones are when the stride is 1; past
+                    // the chunk's end the first ones again, unused)
+                    ldmatrix_x4_trans(tile + (hz ? at : at2) + ((t + 16 * hz) & (kC - 1)) * 128, next);
+                    uint32_t part[3][4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        split3(mul2(m < 2 ? w0 : w1, bf16x2_to_f32x2(v[m])), part[0][m], part[1][m], part[2][m]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        tmem_st_frag8u(dst + ((uint32_t)(hz * 16) << 16) + k * (L::kSlot / 2) + (t & (L::kSlot - 1)) / 2,
+                                       part[k]);
                 }
-#pragma unroll
-                for (int k = 0; k < 3; ++k) tmem_st8u(dst + k * (L::kSlot / 2) + kk * 8, part[k]);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bWFull + (i & 1)));
+            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bWFull + (s & 1)));
         }
     }
 }
 
-// ---- warps 12-13: scores ----------------------------------------------------------------------------------
+// ---- warps 20-23: scores ----------------------------------------------------------------------------------
+// TMEM lanes 64-127 repeat 0-63.  Of the 32 x 32 blocks of scores one is empty, two are cut by the diagonal: the
+// rows with one block share it (16 columns a warp, and as much of the empty one to write), the others take one each.
 template <int kMode>
 GDN_DEVICE void score_role(const Ctx& c) {
     using L = Layout<kMode>;
-    const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;      // 0 or 1
-    const int t = quad * 32 + lane;
+    const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+    const int t = (quad & 1) * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const int32_t total = c.reps * c.chunks;
     const bool bw = c.w.p.backward != 0;
-    for (int32_t it = 0; it < total; ++it) {
-        const int st = it % L::kStages;
-        if (!c.wait(L::kBars, L::bFull + st, it / L::kStages)) return;
+    const bool two = ((quad & 1) == 0) == bw;                   // this row block has two blocks of scores
+    const int first = two ? (quad >> 1) * 32 : (bw ? 32 : 0) + (quad >> 1) * 16;
+    const int empty = (bw ? 0 : 32) + (quad >> 1) * 16;
+    Ring<L::kStages> ring;
+#pragma unroll 1
+    for (int32_t it = 0; it < total; ++it, ring.next()) {
+        const int st = ring.st;
+        if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
         const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
         const int valid = reinterpret_cast<const int32_t*>(gate)[257];
+        // (kExact: the exponents' high and low parts; else one number, whose rounding is far below bf16's)
         const float eh = gate[128 + t], el = gate[192 + t];
-        if (!c.wait(L::kBars, L::bPFull, it)) return;
-        tc_fence_after();
+        const float2 eh2 = make_float2(eh, eh), el2 = make_float2(el, el);
         // the scores of the chunk before have been used
         if (it > 0 && !c.wait(L::kBars, L::bOFull, it - 1)) return;
+        if (!c.wait(L::kBars, L::bPFull, it)) return;
+        tc_fence_after();
         uint8_t* row = c.sm + L::kScores;
+        if (!two) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // the half above (backward: below) the diagonal of this warp's rows is empty
-            const bool empty = bw ? (quad == 1 && half == 0) : (quad == 0 && half == 1);
-            if (empty) {
+            for (int k = 0; k < L::kParts; ++k)
 #pragma unroll
-                for (int k = 0; k < L::kParts; ++k)
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<uint4*>(row + k * kPanel + sw128_off(t, empty / 8 + j)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll 1
+        for (int s = first; s < first + (two ? 32 : 16); s += 16) {
+            float p[16];
+            tmem_ld16w(c.tmem + lanes + L::tP + s, p);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4*>(row + k * kPanel + sw128_off(t, half * 4 + j)) = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-            }
-            float p[32];
-            tmem_ld32w(c.tmem + lanes + L::tP + half * 32, p);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const int s = half * 32 + j;
-                const float4 sh = *reinterpret_cast<const float4*>(gate + 128 + s);
-                float d[4] = {eh - sh.x, eh - sh.y, eh - sh.z, eh - sh.w};
-                const float4 sl = *reinterpret_cast<const float4*>(gate + 192 + s);
-                d[0] += el - sl.x; d[1] += el - sl.y; d[2] += el - sl.z; d[3] += el - sl.w;
+            for (int j = 0; j < 16; j += 4) {
+                const float4 sh = *reinterpret_cast<const float4*>(gate + 128 + s + j);
+                float2 d0 = add2(eh2, make_float2(-sh.x, -sh.y)), d1 = add2(eh2, make_float2(-sh.z, -sh.w));
+                if (kMode == kExact) {
+                    const float4 sl = *reinterpret_cast<const float4*>(gate + 192 + s + j);
+                    d0 = add2(d0, add2(el2, make_float2(-sl.x, -sl.y)));
+                    d1 = add2(d1, add2(el2, make_float2(-sl.z, -sl.w)));
+                }
+                const float d[4] = {d0.x, d0.y, d1.x, d1.y};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool keep = bw ? (s + e >= t && s + e < valid) : (s + e <= t);
+                    const int at = s + j + e;
+                    const bool keep = bw ? (at >= t && at < valid) : (at <= t);
                     p[j + e] = keep ? p[j + e] * exp2_fast(d[e]) : 0.f;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t v[L::kParts][4];
+            for (int j = 0; j < 2; ++j) {
+                uint32_t v[3][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float p0 = p[j * 8 + 2 * e], p1 = p[j * 8 + 2 * e + 1];
-                    if (kMode == kExact) split3(p0, p1, v[0][e], v[L::kParts > 1 ? 1 : 0][e], v[L::kParts > 2 ? 2 : 0][e]);
-                    else v[0][e] = pack_bf16x2(p0, p1);
+                    const float2 x = make_float2(p[8 * j + 2 * e], p[8 * j + 2 * e + 1]);
+                    if (kMode == kExact) split3(x, v[0][e], v[1][e], v[2][e]);
+                    else v[0][e] = pack_bf16x2(x.x, x.y);
                 }
 #pragma unroll
                 for (int k = 0; k < L::kParts; ++k)
-                    *reinterpret_cast<uint4*>(row + k * kPanel + sw128_off(t, half * 4 + j)) =
+                    *reinterpret_cast<uint4*>(row + k * kPanel + sw128_off(t, s / 8 + j)) =
                         make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
             }
         }
+        // the product with z needs its rows behind the part's last token cleared too (the weights' warps clear them
+        // for themselves; the same zeros)
+        if (valid < kC) clear_rows(c.sm + st * L::kStage + L::kZ, valid);
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -487,9 +667,8 @@ GDN_DEVICE void score_role(const Ctx& c) {
     }
 }
 
-// ---- warps 0-7: state and output ----------------------------------------------------------------------------
-// Thread (quad, half, lane): row z = 32 quad + lane of the state, columns 64 half .. + 64; of the output, z index
-// z and the chunk's tokens 32 half .. + 32.
+// ---- warps 0-7: state -----------------------------------------------------------------------------------------
+// Thread (quad, half, lane): row z = 32 quad + lane of the state, columns 64 half .. + 64.
 template <int kMode>
 GDN_DEVICE void put_state(const Ctx& c, uint32_t lanes, int half, const float* S) {
     using L = Layout<kMode>;
@@ -499,7 +678,7 @@ GDN_DEVICE void put_state(const Ctx& c, uint32_t lanes, int half, const float* S
         uint32_t v[3][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (kMode == kExact) split3(S[j + 2 * e], S[j + 2 * e + 1], v[0][e], v[1][e], v[2][e]);
+            if (kMode == kExact) split3(make_float2(S[j + 2 * e], S[j + 2 * e + 1]), v[0][e], v[1][e], v[2][e]);
             else v[0][e] = pack_bf16x2(S[j + 2 * e], S[j + 2 * e + 1]);
         }
 #pragma unroll
@@ -545,132 +724,218 @@ GDN_DEVICE void state_role(const Ctx& c) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, half = warp >> 2;
     const int z = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const int heads = p.Hv / p.out_rep;
-    const float fa = p.backward ? 1.f : p.scale, fp = p.scale;
     float S[64];
-    int32_t it = 0;
+    Ring<L::kStages> ring;
+    uint32_t odd = 0;                           // parity of the chunk
     for (int r = 0; r < c.reps; ++r) {
         const int h = c.head0 + r;
         const int64_t own = ((int64_t)c.part.seq * p.Hv + h) * (kD * kD);
-        const int64_t joint = ((int64_t)(blockIdx.x / (kMode == kState ? p.Hv : heads)) * p.Hv + h) * (kD * kD);
+        const int64_t joint = ((int64_t)c.index * p.Hv + h) * (kD * kD);
         if (kMode == kState) load_state(S, nullptr, false, z, half);
         else if (c.w.split && !c.part.alone) load_state(S, c.w.joint + joint, c.w.joint_t != 0, z, half);
         else load_state(S, p.init ? p.init + own : nullptr, p.state_t != 0, z, half);
-        if (L::kOuts && c.chunks > 0) put_state<kMode>(c, lanes, half, S);
-        for (int32_t n = 0; n < c.chunks; ++n, ++it) {
-            const int st = it % L::kStages;
-            if (!c.wait(L::kBars, L::bFull + st, it / L::kStages)) return;
-            const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
-            const float gamma = gate[256];
-            if (!c.wait(L::kBars, L::bKvFull, it)) return;
-            tc_fence_after();
+        // turn n: the state behind chunk n - 1, and its copy for chunk n
+#pragma unroll 1
+        for (int32_t n = 0; n <= c.chunks; ++n) {
+            if (n > 0) {
+                const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + ring.st * L::kGateBytes);
+                if (!c.wait(L::kBars, L::bFull + ring.st, ring.phase)) return;
+                const float2 gamma2 = make_float2(gate[256], gate[256]);
+                if (!c.wait(L::kBars, L::bKvFull, odd)) return;
+                tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 64; j += 32) {
-                float kv[32];
-                tmem_ld32w(c.tmem + lanes + L::tKv + half * 64 + j, kv);
+                for (int j = 0; j < 64; j += 16) {
+                    float kv[16];
+                    tmem_ld16w(c.tmem + lanes + L::tKv + half * 64 + j, kv);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[j + e] = fmaf(gamma, S[j + e], kv[e]);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bKvFree));
-            if (kMode == kState) {
-                if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
-                continue;
-            }
-            // inter has read the state's bf16 copy, and inter and intra are complete
-            if (!c.wait(L::kBars, L::bOFull, it)) return;
-            tc_fence_after();
-            if (n + 1 < c.chunks) put_state<kMode>(c, lanes, half, S);
-            const int64_t t0 = c.chunk_start(n);
-            const int valid = (int)min((int64_t)kC, c.part.t1 - t0);
-#pragma unroll
-            for (int b = 0; b < 32; b += 16) {
-                const int tb = half * 32 + b;
-                float inter[16], out[16];
-                tmem_ld16x2w(c.tmem + lanes + L::tInter + tb, c.tmem + lanes + L::tIntra + tb, inter, out);
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(gate + tb + e);
-                    out[e] = fmaf(fa * a.x, inter[e], fp * out[e]);
-                    out[e + 1] = fmaf(fa * a.y, inter[e + 1], fp * out[e + 1]);
-                    out[e + 2] = fmaf(fa * a.z, inter[e + 2], fp * out[e + 2]);
-                    out[e + 3] = fmaf(fa * a.w, inter[e + 3], fp * out[e + 3]);
-                }
-                const int64_t row = ((t0 + tb) * heads + c.head) * kD + z;
-                const int64_t step = (int64_t)heads * kD;
-                const int rows = valid - tb;
-                if (kMode == kExact) {
-                    // u_t . out_t over the warp's 32 z indices: at each step lanes m apart exchange the half
-                    // of their sums that the other one keeps
-                    float dot[16];
-                    const uint8_t* u = c.sm + st * L::kStage + L::kU + (z >> 6) * kPanel + (z & 7) * 2;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int t = tb + e;
-                        const float uv = bf16_to_f32(*reinterpret_cast<const uint16_t*>(u + sw128_off(t, (z & 63) >> 3)));
-                        dot[e] = uv * out[e];
-                    }
-#pragma unroll
-                    for (int m = 1, hf = 8; hf >= 1; m <<= 1, hf >>= 1)
-#pragma unroll
-                        for (int e = 0; e < hf; ++e) {
-                            const float give = (lane & m) ? dot[e] : dot[e + hf];
-                            const float keep = (lane & m) ? dot[e + hf] : dot[e];
-                            dot[e] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-                        }
-                    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 16);
-                    const int e = ((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | ((lane & 8) >> 3);
-                    if (lane < 16)
-                        reinterpret_cast<float*>(c.sm + L::kDots)[warp * 32 + b + e] = dot[0];
-                }
-                if (p.out_rep > 1) {
-                    float* acc = p.out_bf16 ? p.acc : static_cast<float*>(p.out);
-                    if (r > 0)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (e < rows) out[e] += acc[row + e * step];
-                    if (r + 1 < c.reps) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (e < rows) acc[row + e * step] = out[e];
-                        continue;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 x = fma2(gamma2, make_float2(S[j + e], S[j + e + 1]), make_float2(kv[e], kv[e + 1]));
+                        S[j + e] = x.x;
+                        S[j + e + 1] = x.y;
                     }
                 }
-                if (p.out_bf16) {
-                    uint16_t* o = static_cast<uint16_t*>(p.out) + row;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (e < rows) o[e * step] = (uint16_t)f32_to_bf16_bits(out[e]);
-                } else {
-                    float* o = static_cast<float*>(p.out) + row;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (e < rows) o[e * step] = out[e];
-                }
-            }
-            tc_fence_before();
-            if (kMode == kExact) {
-                // (the next chunk's sums are written after every warp has arrived below)
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bDots + half));
-                if (!c.wait(L::kBars, L::bDots + half, it)) return;
-                if (quad == 0 && half * 32 + lane < valid) {
-                    const float* d = reinterpret_cast<const float*>(c.sm + L::kDots) + half * 128 + lane;
-                    p.dots[(int64_t)h * p.T + t0 + half * 32 + lane] = (d[0] + d[32]) + (d[64] + d[96]);
+                if (lane == 0) {
+                    mbar_arrive(c.bar(L::kBars, L::bKvFree));
+                    mbar_arrive(c.bar(L::kBars, L::bEmpty + ring.st));
+                }
+                ring.next();
+                // inter has read the copy for the chunk before
+                if (L::kOuts && !c.wait(L::kBars, L::bOFull, odd)) return;
+                odd ^= 1u;
+            }
+            if (L::kOuts && n < c.chunks) put_state<kMode>(c, lanes, half, S);
+        }
+        if (kMode == kState) store_state(S, c.w.joint + joint, false, z, half);
+        else if (p.fin && c.part.last) store_state(S, p.fin + own, p.state_t != 0, z, half);
+    }
+}
+
+// ---- warps 8-15: output -----------------------------------------------------------------------------------------
+// Warp (quad, half): z indices 32 quad .. + 32, tokens 32 half .. + 32.
+template <int kMode>
+GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
+    using L = Layout<kMode>;
+    const LinPass& p = c.w.p;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 8, quad = warp & 3, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const int heads = p.Hv / p.out_rep;
+    const float2 fa2 = p.backward ? make_float2(1.f, 1.f) : make_float2(p.scale, p.scale);
+    const float2 fp2 = make_float2(p.scale, p.scale);
+    const bool f32 = p.out_rep > 1 || !p.out_bf16;
+    const uint32_t rows = L::kHalf * half;      // of a stage: where the output is staged, over x, whose products are done
+    Ring<L::kStages> ring;
+    uint32_t odd = 0;                           // parity of the chunk
+    int held = -1;                              // the stage whose rows are leaving
+    for (int r = 0; r < c.reps; ++r) {
+#pragma unroll 1
+        for (int32_t n = 0; n < c.chunks; ++n) {
+            const int st = ring.st;
+            const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
+            if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
+            const int64_t t0 = c.chunk_start(n);
+            const int valid = reinterpret_cast<const int32_t*>(gate)[257];
+            if (!c.wait(L::kBars, L::bOFull, odd)) return;
+            tc_fence_after();
+            if (held >= 0 && lane == 0) {       // the chunk before's rows have left its stage
+                bulk_wait_read();
+                mbar_arrive(c.bar(L::kBars, L::bEmpty + held));
+            }
+            held = -1;
+            // The fragment layout of transposed 8 x 8 matrices: tokens tq + 8 j (+ 1), z indices 32 quad + 16 hz +
+            // lane / 4 (+ 8)
+            const int tq = 2 * (lane & 3);
+            const uint32_t stage = c.base + st * L::kStage;
+            // matrix m of 16 tokens and 16 z indices: tokens 8 (m >> 1), z indices 8 (m & 1)
+            const int mt = ((lane >> 4) << 3) + (lane & 7), mz = quad * 32 + ((lane >> 3) & 1) * 8;
+#pragma unroll 1
+            for (int tb = 0; tb < 32; tb += 16) {
+                const float2 a0 = mul2(fa2, *reinterpret_cast<const float2*>(gate + half * 32 + tb + tq));
+                const float2 a1 = mul2(fa2, *reinterpret_cast<const float2*>(gate + half * 32 + tb + tq + 8));
+                float dot[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int hz = 0; hz < 32; hz += 16) {
+                    float inter[8], out[8];
+                    const uint32_t src = c.tmem + lanes + ((uint32_t)hz << 16) + half * 32 + tb;
+                    tmem_ld_frag16x2w(src + L::tInter, src + L::tIntra, inter, out);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 x = fma2(e < 4 ? a0 : a1, make_float2(inter[e], inter[e + 1]),
+                                              mul2(fp2, make_float2(out[e], out[e + 1])));
+                        out[e] = x.x;
+                        out[e + 1] = x.y;
+                    }
+                    const int zm = mz + hz, tm = tb + mt;               // this lane's row of a matrix, of the half
+                    if (kMode == kExact) {
+                        uint32_t u[4];
+                        ldmatrix_x4_trans(stage + L::kU + (zm >> 6) * kPanel + sw128_off(half * 32 + tm, (zm & 63) >> 3), u);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float2 f = bf16x2_to_f32x2(u[m]);
+                            const int g = m >> 1;                       // the 8-token group
+                            dot[2 * g] = fmaf(f.x, out[2 * m], dot[2 * g]);
+                            dot[2 * g + 1] = fmaf(f.y, out[2 * m + 1], dot[2 * g + 1]);
+                        }
+                    }
+                    if (f32) {
+                        // (conflict-free: a warp's rows put their 16-byte pieces in different places)
+                        uint8_t* to = c.sm + st * L::kStage + rows + quad * L::kRows;
+                        const int piece = (hz + (lane >> 2)) >> 2;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float*>(to + sw128_off(tb + tq + (e >> 2) * 8 + (e & 1), piece + ((e >> 1) & 1) * 2) +
+                                                      ((lane >> 2) & 3) * 4) = out[e];
+                    } else {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) v[m] = pack_bf16x2(out[2 * m], out[2 * m + 1]);
+                        stmatrix_x4_trans(stage + rows + (zm >> 6) * L::kRows + sw128_off(tm, (zm & 63) >> 3), v);
+                    }
+                }
+                if (kMode == kExact) {
+                    // u_t . out_t over this warp's 32 z indices: lanes of one lane % 4 hold the same tokens; lanes
+                    // m apart exchange the half of their sums that the other one keeps
+                    const float g0 = lane & 4 ? dot[0] : dot[2], g1 = lane & 4 ? dot[1] : dot[3];
+                    float k0 = lane & 4 ? dot[2] : dot[0], k1 = lane & 4 ? dot[3] : dot[1];
+                    k0 += __shfl_xor_sync(0xffffffffu, g0, 4);
+                    k1 += __shfl_xor_sync(0xffffffffu, g1, 4);
+                    const float g2 = lane & 8 ? k0 : k1;
+                    float k2 = lane & 8 ? k1 : k0;
+                    k2 += __shfl_xor_sync(0xffffffffu, g2, 8);
+                    k2 += __shfl_xor_sync(0xffffffffu, k2, 16);
+                    if (lane < 16)
+                        reinterpret_cast<float*>(c.sm + L::kDots)[odd * 256 + warp * 32 + tb + (lane & 4) * 2 +
+                                                                  2 * (lane & 3) + (lane >> 3)] = k2;
                 }
             }
+            tc_fence_before();
+            fence_async_smem();
+            const bool whole = half * 32 + 32 <= valid;         // every row of this half is this part's
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(c.bar(L::kBars, L::bOFree));
-                mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
+                mbar_arrive(c.bar(L::kBars, L::bRows + half));
+                if (whole && quad != 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
             }
+            const uint32_t now = odd;
+            ring.next();
+            odd ^= 1u;
+            if (whole && quad != 0) continue;
+            // the four warps of this half have their z indices in place
+            if (!c.wait(L::kBars, L::bRows + half, now)) return;
+            if (whole) {
+                if (lane == 0) {
+                    const int32_t x = c.head * kD, y = (int32_t)t0 + half * 32;
+                    const uint32_t from = stage + rows;
+                    if (!f32) {
+                        tma_store_2d(mo, x, y, from);
+                        tma_store_2d(mo, x + 64, y, from + L::kRows);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            if (r == 0) tma_store_2d(mo, x + 32 * k, y, from + k * L::kRows);
+                            else tma_add_2d(mo, x + 32 * k, y, from + k * L::kRows);
+                        }
+                    }
+                    bulk_commit();
+                }
+                held = st;
+            } else {
+                // the part's last rows: those behind them are not this part's, so plain stores, 8 rows a warp
+                const int pieces = f32 ? 32 : 16;
+                float* o32 = p.out_bf16 ? p.acc : static_cast<float*>(p.out);
+#pragma unroll 1
+                for (int i = lane; i < 8 * pieces; i += 32) {
+                    const int row = quad * 8 + i / pieces, piece = i % pieces;
+                    if (half * 32 + row >= valid) break;
+                    const int64_t at = ((t0 + half * 32 + row) * heads + c.head) * kD;
+                    uint4 v = *reinterpret_cast<const uint4*>(c.sm + st * L::kStage + rows + (piece >> 3) * L::kRows +
+                                                              sw128_off(row, piece & 7));
+                    if (!f32) {
+                        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at)[piece] = v;
+                    } else {
+                        float4* to = reinterpret_cast<float4*>(o32 + at) + piece;
+                        float4 x = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+                        if (r > 0) {
+                            const float4 y = *to;
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        *to = x;
+                    }
+                }
+            }
+            if (kMode == kExact && quad == 0 && half * 32 + lane < valid) {
+                // (two buffers: the chunk after the next needs this stage, which this warp has not yet released)
+                static_assert(kMode != kExact || L::kStages == 2, "the buffers of the dot products");
+                const float* d = reinterpret_cast<const float*>(c.sm + L::kDots) + now * 256 + half * 128 + lane;
+                p.dots[(int64_t)(c.head0 + r) * p.T + t0 + half * 32 + lane] = (d[0] + d[32]) + (d[64] + d[96]);
+            }
+            __syncwarp();
+            if (!whole && lane == 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
         }
-        if (kMode == kState) {
-            store_state(S, c.w.joint + joint, false, z, half);
-        } else if (p.fin && c.part.last) {
-            store_state(S, p.fin + own, p.state_t != 0, z, half);
-        }
+        // this head's rows are in place before the next head adds to them
+        bulk_wait();
     }
 }
 
@@ -678,7 +943,7 @@ template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                 const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mu,
-                const __grid_constant__ Walk w) {
+                const __grid_constant__ CUtensorMap mo, const __grid_constant__ Walk w) {
     using L = Layout<kMode>;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -694,10 +959,10 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         auto init = [&](int i, uint32_t n) { mbar_init(base + L::kBars + i * 8, n); };
         for (int s = 0; s < L::kStages; ++s) {
             init(L::bFull + s, 2);                  // the loads' bytes; the decays
-            init(L::bEmpty + s, 1 + 8);             // the products; warps 0-7
+            init(L::bEmpty + s, kMode == kState ? 1 + 8 : 2 + 8 + 8);       // the products; warps 0-7; warps 8-15
         }
         init(L::bPFull, 1);
-        init(L::bPReady, 2);
+        init(L::bPReady, 4);
         init(L::bAReady, 8);
         init(L::bKvFull, 1);
         init(L::bKvFree, 8);
@@ -707,48 +972,66 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
             init(L::bWFull + s, 4);
             init(L::bWFree + s, 1);
         }
-        init(L::bZeroed, 4);
-        init(L::bDots, 4);
-        init(L::bDots + 1, 4);
+        init(L::bZeroed, kMode == kState ? 8 : 4);
+        init(L::bRows, 4);
+        init(L::bRows + 1, 4);
         init(L::bDrain, 1);
+        init(L::bDrain + 1, 1);
+        init(L::bDone, 27);
         *abort = 0;
         fence_mbar_init();
     }
-    if (warp == 15) tmem_alloc(base + L::kMisc, 512);
+    if (warp == 25) tmem_alloc(base + L::kMisc, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kMisc);
     const int head = (int)(blockIdx.x - (unsigned)index * heads);
     const int reps = kMode == kState ? 1 : w.p.out_rep;
-    const Ctx c{w, sm, base, tmem, abort, part, (int32_t)((part.t1 - part.t0 + kC - 1) / kC), head, reps, head * reps};
+    const Ctx c{w, sm, base, tmem, abort, base + L::kMisc + 8, part, index, (int32_t)((part.t1 - part.t0 + kC - 1) / kC), head, reps, head * reps};
     if (warp < 8) {
+        regs_inc<kRegsState>();
         state_role<kMode>(c);
-    } else if (warp < 12) {
-        weight_role<kMode>(c);
-    } else if (warp < 14) {
-        if (kMode != kState) score_role<kMode>(c);
-    } else if (warp == 14) {
-        load_role<kMode>(c, &mx, &my, &mz, &mu);
+    } else if (warp < 16) {
+        regs_dec<kRegsOut>();
+        if (L::kOuts) out_role<kMode>(c, &mo);
+        bulk_wait();                            // rows still leaving (a role that gave up)
+    } else if (warp < 20) {
+        weight_role<kMode>(c, 0, kMode == kState ? 2 : 1);
+    } else if (warp < 24) {
+        regs_dec<kRegsScores>();
+        if (kMode == kState) weight_role<kMode>(c, 1, 2);
+        else score_role<kMode>(c);
     } else {
-        mma_role<kMode>(c);
-    }
-    if (kMode == kState && warp == 13) {
-        // the part's whole decay
-        double sum = 0.0;
-        for (int64_t t = part.t0 + (threadIdx.x & 31); t < part.t1; t += 32) {
-            const float g = w.p.g[t * w.p.ldg + head];
-            sum += g < kLinMinLogDecay ? kLinMinLogDecay : g;
-        }
+        regs_dec<kRegsRest>();
+        if (warp == 24) load_role<kMode>(c, &mx, &my, &mz, &mu);
+        if (warp == 25) kv_role<kMode>(c);
+        if (warp == 26 && L::kOuts) out_products_role<kMode>(c);
+        if (warp == 26 && kMode == kState) {
+            // the part's whole decay
+            double sum = 0.0;
+            for (int64_t t = part.t0 + (threadIdx.x & 31); t < part.t1; t += 32) {
+                const float g = w.p.g[t * w.p.ldg + head];
+                sum += g < kLinMinLogDecay ? kLinMinLogDecay : g;
+            }
 #pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if ((threadIdx.x & 31) == 0) w.joint_decay[(int64_t)index * w.p.Hv + head] = (float)exp(sum);
+            for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if ((threadIdx.x & 31) == 0) w.joint_decay[(int64_t)index * w.p.Hv + head] = (float)exp(sum);
+        }
+        if (warp == 27) {
+            decay_role<kMode>(c);
+            mbar_wait(c.bar(L::kBars, L::bDone), 0, c.abort, kWaitLimitNs);
+        }
+    }
+    if (warp != 27) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(base + L::kBars + L::bDone * 8);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (*abort && threadIdx.x == 0) *w.err = 1u;
-    if (warp == 15) tmem_dealloc(tmem, 512);
+    if (warp == 25) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace lin

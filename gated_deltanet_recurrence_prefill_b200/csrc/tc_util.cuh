@@ -87,6 +87,27 @@ TC_DEVICE bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, uin
     }
 }
 
+// Wait that gives up only when *abort is set: a watchdog elsewhere in the CTA bounds it.  A few instructions, for
+// kernels of many roles whose code competes for the instruction cache.
+// (The loop is in PTX because the same in C++ took 110 cycles a wait on a completed phase, this 40.)
+TC_DEVICE bool mbar_wait_watched(uint32_t bar, uint32_t parity, uint32_t abort) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a;\n"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "ld.volatile.shared.u32 a, [%3];\n\t"
+        "setp.eq.u32 q, a, 0;\n\t"
+        "@q bra TRY;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(abort)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait on a barrier that threads of another CTA of the cluster arrive on
 // (acquire at cluster scope, so that their released writes are visible).
 TC_DEVICE bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns = 20000) {
@@ -231,6 +252,14 @@ TC_DEVICE void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int3
 // thread's bulk async-groups
 TC_DEVICE void tma_store_2d(const CUtensorMap* map, int32_t x, int32_t y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+// the same, added in float32 to what is there
+TC_DEVICE void tma_add_2d(const CUtensorMap* map, int32_t x, int32_t y, uint32_t src) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y), "r"(src)
                  : "memory");
@@ -399,24 +428,56 @@ TC_DEVICE void tmem_ld32w(uint32_t taddr, float* v) {
         : "memory");
 }
 
-// two 16-column loads and the wait for both
-TC_DEVICE void tmem_ld16x2w(uint32_t taddr_a, uint32_t taddr_b, float* va, float* vb) {
+// 16 columns and the wait
+TC_DEVICE void tmem_ld16w(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// two loads of 16 lanes x 16 columns and the wait for both.  Of the 8-column group j, thread l holds
+// row l / 4, columns 2 (l % 4) and + 1 in v[4 j] and v[4 j + 1], row l / 4 + 8 in v[4 j + 2] and v[4 j + 3]
+// (the fragment layout of an 8 x 8 matrix of pairs)
+TC_DEVICE void tmem_ld_frag16x2w(uint32_t taddr_a, uint32_t taddr_b, float* va, float* vb) {
     uint32_t* a = reinterpret_cast<uint32_t*>(va);
     uint32_t* b = reinterpret_cast<uint32_t*>(vb);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
-          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]),
-          "=r"(a[15]),
-          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
-          "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]),
-          "=r"(b[15])
+          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7])
         : "r"(taddr_a), "r"(taddr_b)
         : "memory");
+}
+
+// 16 lanes x 8 columns: of the 4-column group j, thread l's words go to row l / 4 (r[2 j]) and row
+// l / 4 + 8 (r[2 j + 1]), column l % 4
+TC_DEVICE void tmem_st_frag8u(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+// four transposed 8 x 8 matrices of 16-bit elements, lane l giving the address of row l % 8 of matrix l / 8:
+// thread l holds of each the elements (row 2 (l % 4), column l / 4) and (row 2 (l % 4) + 1, column l / 4)
+TC_DEVICE void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+TC_DEVICE void stmatrix_x4_trans(uint32_t addr, const uint32_t* r) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 TC_DEVICE void tmem_st32(uint32_t taddr, const float* v) {
@@ -456,6 +517,13 @@ TC_DEVICE void tmem_st4u(uint32_t taddr, const uint32_t* r) {
 }
 
 TC_DEVICE void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- registers of a warpgroup ---------------------------------------------------
+// every warp of four consecutive ones executes it; all shares together stay within the launch's
+template <int kRegs>
+TC_DEVICE void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+TC_DEVICE void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 // ---- named barriers ------------------------------------------------------------
 
