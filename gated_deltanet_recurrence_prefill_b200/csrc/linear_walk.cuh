@@ -31,12 +31,12 @@
 //
 // Roles in a CTA of 28 warps, handing over through mbarriers:
 //   warps 0-7    the state in registers (64 columns a thread), its bf16 copy
-//   warps 8-15   the output: the chunk's inter and intra
+//   warps 8-15   the output: the chunk's inter and intra   (kState: one of them, decays)
 //   warps 16-19  w z in three parts (kState: the even slots)
 //   warps 20-23  the scores         (kState: w z, the odd slots)
 //   warp  24     TMA loads
 //   warp  25     issues KV's products
-//   warp  26     issues the others
+//   warp  26     issues the others   (kState: every other chunk's)
 //   warp  27     the chunk's decays; it waits for every stage to come round, and for
 //                the other roles to end, at most two seconds each, and makes every
 //                other wait give up when that is over (the error word is raised)
@@ -161,25 +161,27 @@ struct Layout {
     static constexpr uint32_t kGateBytes = (4 * 64 + 4) * 4;
     static constexpr uint32_t kDots = kGates + kStages * kGateBytes;       // [2][8 warps][32] partial dot products
     static constexpr uint32_t kBars = kDots + (kMode == kExact ? 2 * 8 * 32 * 4 : 0);
+    // the scores, and intra in their place, in one or two sets of columns; KV too
+    static constexpr int kPSets = kMode == kOut ? 2 : 1, kKvSets = kMode == kState ? 2 : 1;
+    // w z is handed over in slots of this many tokens
+    static constexpr int kSlot = kMode == kState ? 32 : 16;
+    static constexpr int kSlots = kC / kSlot;
+    static constexpr int kSlotBufs = kMode == kExact ? 2 : 4;
+    static constexpr uint32_t kSlotCols = 3 * kSlot / 2;
     // barriers
     static constexpr int bFull = 0, bEmpty = bFull + kStages, bPFull = bEmpty + kStages, bPReady = bPFull + 1,
-                         bAReady = bPReady + 1, bKvFull = bAReady + 1, bKvFree = bKvFull + 1, bOFull = bKvFree + 1,
-                         bOFree = bOFull + 1, bWFull = bOFree + 1, bWFree = bWFull + 2, bZeroed = bWFree + 2,
+                         bAReady = bPReady + 1, bKvFull = bAReady + 1, bKvFree = bKvFull + 2, bOFull = bKvFree + 2,
+                         bOFree = bOFull + 1, bWFull = bOFree + 1, bWFree = bWFull + kSlotBufs, bZeroed = bWFree + kSlotBufs,
                          bRows = bZeroed + 1, bDrain = bRows + 2, bDone = bDrain + 2, kBarCount = bDone + 1;
-    static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag
+    static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag, a part's decay
     static constexpr uint32_t kSmem = kMisc + 64;
     static constexpr uint32_t kAlloc = kSmem + 1024;
     static_assert(kAlloc <= 232448, "a CTA's shared memory");
-    // TMEM columns.  kExact: intra takes the scores' columns once they have been read.
-    static constexpr uint32_t tKv = 0, tInter = 128, tP = 192, tIntra = kMode == kExact ? 192 : 256,
-                              tA = kMode == kExact ? 256 : 320, tW = kMode == kExact ? 448 : 384;
-    // w z is handed over in slots of this many tokens, two slots
-    static constexpr int kSlot = kMode == kExact ? 16 : 32;
-    static constexpr int kSlots = kC / kSlot;
-    static constexpr uint32_t kSlotCols = 3 * kSlot / 2;
+    // TMEM columns.  Intra takes the scores' columns once they have been read.
+    static constexpr uint32_t tKv = 0, tInter = kKvSets * 128, tP = tInter + 64, tA = tP + kPSets * 64,
+                              tW = kMode == kState ? tInter : tA + kParts * 64;
+    static_assert(tW + kSlotBufs * kSlotCols <= 512, "TMEM columns");
 };
-static_assert(Layout<kExact>::tW + 2 * Layout<kExact>::kSlotCols <= 512 && Layout<kOut>::tW + 2 * Layout<kOut>::kSlotCols <= 512,
-              "TMEM columns");
 
 // pairs of float32 operations in one instruction
 GDN_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
@@ -258,6 +260,11 @@ struct Ctx {
     GDN_DEVICE bool wait(uint32_t bars, int i, uint32_t parity) const {
         return mbar_wait_watched(bar(bars, i), parity & 1u, abort_at);
     }
+    // the it-th use of a barrier, or of kSets barriers in turn
+    template <int kSets>
+    GDN_DEVICE bool wait_set(uint32_t bars, int i, uint32_t it) const {
+        return kSets == 2 ? wait(bars, i + (int)(it & 1u), it >> 1) : wait(bars, i, it);
+    }
     // first token of the n-th chunk in the pass's direction
     GDN_DEVICE int64_t chunk_start(int32_t n) const {
         return part.t0 + (int64_t)(w.p.backward ? chunks - 1 - n : n) * kC;
@@ -311,55 +318,81 @@ out:
 }
 
 // ---- warp 27: decays -----------------------------------------------------------------------------------
-// Sums of log decays to base 2 in fixed point, 2^-32 a step (64 tokens of at most 151 fit 46 bits): exact sums
-// and differences, one integer add a step.
+// Sums of log decays to base 2 as two integers, multiples of 2^-10 and of 2^-32 (a token's high part is below 151 *
+// 2^10, its low part at most 2^21): every sum and difference in a chunk is exact, at one 32-bit addition each.
+// kState: two warps take the chunks in turn (one alone, at 1,300 cycles a chunk, was the slowest role).
 template <int kMode>
-GDN_DEVICE void decay_role(const Ctx& c) {
+GDN_DEVICE void decay_role(const Ctx& c, int which, int stride) {
     using L = Layout<kMode>;
     const int lane = threadIdx.x & 31;
     const LinPass& p = c.w.p;
     const bool bw = p.backward != 0;
     const float ws = bw ? p.scale : 1.f;
     const int i0 = 2 * lane, i1 = i0 + 1;                       // this lane's tokens
-    auto fixed = [](float g) {
+    auto split = [](float g, int& hi, int& lo) {
         // exp of what is beyond these limits is 0 or inf in float32
         g = g < kLinMinLogDecay ? kLinMinLogDecay : g > -kLinMinLogDecay ? -kLinMinLogDecay : g;
-        return __double2ll_rn((double)g * (1.4426950408889634 * 4294967296.0));
+        // g log2(e), the constant in two parts
+        const float x = g * 1.44269502f;
+        const float rest = fmaf(g, 1.44269502f, -x) + g * 1.92596303e-8f;
+        hi = __float2int_rn(x * 1024.f);
+        lo = __float2int_rn((fmaf((float)hi, -1.f / 1024.f, x) + rest) * 4294967296.f);
     };
-    auto high = [](long long x) { return (float)(int)(x >> 22) * (1.f / 1024.f); };             // a multiple of 2^-10
-    auto low = [](long long x) { return (float)(int)(x & 0x3fffff) * (1.f / 4294967296.f); };   // the rest, >= 0
+    auto high = [](int x) { return (float)x * (1.f / 1024.f); };
+    auto low = [](int x) { return (float)x * (1.f / 4294967296.f); };
     Ring<L::kStages> ring;
-    int32_t it = 0;
+    if (which == 1) ring.next();
+    int32_t it = which;
+    long long whole = 0;                        // kState: the sum over this warp's chunks, multiples of 2^-32
+    float whole_bad = 0.f;
     for (int r = 0; r < c.reps; ++r) {
-        // this lane's log decays of a chunk, fetched a chunk ahead
-        const int64_t step = (int64_t)(bw ? -kC : kC);
-        int64_t t = c.chunk_start(0);
+        // this lane's log decays, fetched two chunks ahead
+        const int64_t step = (int64_t)(bw ? -kC : kC) * stride;
+        int64_t t = c.chunk_start(which), ahead = t;
         const float* g = p.g + c.head0 + r + (t + i0) * p.ldg;
-        float n0 = t + i0 < c.part.t1 && c.chunks > 0 ? g[0] : 0.f, n1 = t + i1 < c.part.t1 && c.chunks > 0 ? g[p.ldg] : 0.f;
+        int32_t left = c.chunks - which;                        // not yet fetched
+        auto fetch = [&](float& a, float& b) {
+            a = left > 0 && ahead + i0 < c.part.t1 ? g[0] : 0.f;
+            b = left > 0 && ahead + i1 < c.part.t1 ? g[p.ldg] : 0.f;
+            left -= stride;
+            ahead += step;
+            g += step * p.ldg;
+        };
+        float n0, n1, m0, m1;
+        fetch(n0, n1);
+        fetch(m0, m1);
 #pragma unroll 1
-        for (int32_t n = 0; n < c.chunks; ++n, ++it, ring.next()) {
+        for (int32_t n = which; n < c.chunks; n += stride, it += stride, t += step) {
             const float g0 = n0, g1 = n1;
             const int valid = (int)min((int64_t)kC, c.part.t1 - t);
-            t += step;
-            g += step * p.ldg;
-            n0 = n + 1 < c.chunks && t + i0 < c.part.t1 ? g[0] : 0.f;
-            n1 = n + 1 < c.chunks && t + i1 < c.part.t1 ? g[p.ldg] : 0.f;
+            n0 = m0;
+            n1 = m1;
+            fetch(m0, m1);
             // a NaN reaches every sum that has its token
             const unsigned nan0 = __ballot_sync(0xffffffffu, g0 != g0), nan1 = __ballot_sync(0xffffffffu, g1 != g1);
             const unsigned earlier = (1u << lane) - 1u;
-            const long long d1 = fixed(g1);
-            long long G1 = fixed(g0) + d1;
-#pragma unroll 1
+            int h0, l0, h1, l1;
+            split(g0, h0, l0);
+            split(g1, h1, l1);
+            int H1 = h0 + h1, L1 = l0 + l1;
+#pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, G1, m);
-                if (lane >= m) G1 += x;
+                const int x = __shfl_up_sync(0xffffffffu, H1, m), y = __shfl_up_sync(0xffffffffu, L1, m);
+                H1 += lane >= m ? x : 0;
+                L1 += lane >= m ? y : 0;
             }
-            const long long G0 = G1 - d1, all = __shfl_sync(0xffffffffu, G1, 31);
+            const int H0 = H1 - h1, L0 = L1 - l1;
+            const int allH = __shfl_sync(0xffffffffu, H1, 31), allL = __shfl_sync(0xffffffffu, L1, 31);
             const float bad = (nan0 | nan1) ? __int_as_float(0x7fc00000) : 0.f;          // added where a NaN counts
+            if (kMode == kState) {
+                whole += ((long long)allH << 22) + allL;
+                whole_bad += bad;
+            }
             const float bad0 = (((nan0 | nan1) & earlier) | (nan0 & (1u << lane))) ? bad : 0.f;
             const float bad1 = (bad0 != bad0 || (nan1 & (1u << lane))) ? bad : 0.f;
-            const float e0 = exp2_fast(high(G0) + low(G0) + bad0), e1 = exp2_fast(high(G1) + low(G1) + bad1);
-            const float f0 = exp2_fast(high(all - G0) + low(all - G0) + bad), f1 = exp2_fast(high(all - G1) + low(all - G1) + bad);
+            const float e0 = exp2_fast(high(H0) + low(L0) + bad0), e1 = exp2_fast(high(H1) + low(L1) + bad1);
+            const float f0 = exp2_fast(high(allH - H0) + low(allL - L0) + bad);
+            const float f1 = exp2_fast(high(allH - H1) + low(allL - L1) + bad);
             // (the bound of all waits of the CTA: a stage comes round within kWaitLimitNs)
             if (it >= L::kStages &&
                 !mbar_wait(c.bar(L::kBars, L::bEmpty + ring.st), ring.phase ^ 1u, c.abort, kWaitLimitNs))
@@ -370,16 +403,21 @@ GDN_DEVICE void decay_role(const Ctx& c) {
                                                                      i1 < valid ? ws * (bw ? e1 : f1) : 0.f);
             // the exponent of Gamma_ts is E_t - E_s; kExact: high parts (whose differences are exact) and low ones
             const float sg = bw ? -1.f : 1.f;
-            const float l0 = kMode == kExact ? 0.f : low(G0), l1 = kMode == kExact ? 0.f : low(G1);
-            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * (high(G0) + l0) + bad0, sg * (high(G1) + l1) + bad1);
-            if (kMode == kExact) reinterpret_cast<float2*>(gate + 192)[lane] = make_float2(sg * low(G0), sg * low(G1));
+            const float x0 = kMode == kExact ? high(H0) : high(H0) + low(L0), x1 = kMode == kExact ? high(H1) : high(H1) + low(L1);
+            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * x0 + bad0, sg * x1 + bad1);
+            if (kMode == kExact) reinterpret_cast<float2*>(gate + 192)[lane] = make_float2(sg * low(L0), sg * low(L1));
             if (lane == 31) {
                 gate[256] = e1;                                 // the whole chunk's decay
                 reinterpret_cast<int32_t*>(gate)[257] = valid;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bFull + ring.st));
+            for (int k = 0; k < stride; ++k) ring.next();
         }
+    }
+    if (kMode == kState && lane == 0) {
+        reinterpret_cast<long long*>(c.sm + L::kMisc + 16)[which] = whole;
+        reinterpret_cast<float*>(c.sm + L::kMisc + 32)[which] = whole_bad;
     }
 }
 
@@ -401,26 +439,30 @@ GDN_DEVICE void drain(const Ctx& c, uint32_t bar) {
     mbar_wait(bar, 0, &no_abort, kWaitLimitNs);
 }
 
-// KV = (w z)^T y, slot by slot
+// KV = (w z)^T y, slot by slot.  kState: two threads take the chunks in turn, one set of columns each, so that the
+// tensor core has the other's products while one waits and commits.
 template <int kMode>
-GDN_DEVICE void kv_role(const Ctx& c) {
+GDN_DEVICE void kv_role(const Ctx& c, int which) {
     using L = Layout<kMode>;
     if ((threadIdx.x & 31) != 0) return;
     constexpr uint32_t idKv = idesc_bf16(128, 128, false, true);
     const int32_t total = c.reps * c.chunks;
+    constexpr int kKvSets = L::kKvSets;
     Ring<L::kStages> ring;
-    uint32_t odd = 0;                           // parity of the chunk, and of the uses of the barriers once a chunk
     bool ok = true;
+    if (which == 1) ring.next();
 #pragma unroll 1
-    for (int32_t it = 0; it < total; ++it, ring.next(), odd ^= 1u) {
+    for (int32_t it = which; it < total; it += kKvSets) {
         if (!c.wait(L::kBars, L::bFull + ring.st, ring.phase)) break;
-        // the accumulator has been read for the chunk before
-        if (it > 0 && !c.wait(L::kBars, L::bKvFree, odd ^ 1u)) break;
+        // the accumulator has been read for the chunk that used it last
+        if (it >= kKvSets && !c.template wait_set<kKvSets>(L::kBars, L::bKvFree, it - kKvSets)) break;
+        const int set = kKvSets == 2 ? it & 1 : 0;
         const uint64_t dy = mn_major<kMode>(c, ring.st, L::kY);
+        const uint32_t d = c.tmem + L::tKv + set * 128;
 #pragma unroll
         for (int s = 0; s < L::kSlots; ++s) {
-            // use number it * kSlots / 2 + s / 2 of the slot's barriers
-            ok = c.wait(L::kBars, L::bWFull + (s & 1), L::kSlots == 2 ? odd : (uint32_t)(s >> 1));
+            const int use = it * L::kSlots + s, buf = use % L::kSlotBufs;
+            ok = c.wait(L::kBars, L::bWFull + buf, use / L::kSlotBufs);
             if (!ok) break;
             tc_fence_after();
             // smallest part first: the accumulator's rounding is then that of the largest part alone
@@ -428,20 +470,20 @@ GDN_DEVICE void kv_role(const Ctx& c) {
             for (int part = 2; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < L::kSlot / 16; ++kk)
-                    mma_bf16_ta(c.tmem + L::tKv,
-                                c.tmem + L::tW + (s & 1) * L::kSlotCols + part * (L::kSlot / 2) + kk * 8,
+                    mma_bf16_ta(d, c.tmem + L::tW + buf * L::kSlotCols + part * (L::kSlot / 2) + kk * 8,
                                 dy + (s * (L::kSlot / 16) + kk) * 128, idKv, s > 0 || part < 2 || kk > 0);
-            commit_to(c, L::kBars, L::bWFree + (s & 1));
+            commit_to(c, L::kBars, L::bWFree + buf);
         }
         if (!ok) break;
-        commit_to(c, L::kBars, L::bKvFull);
+        commit_to(c, L::kBars, L::bKvFull + set);
         commit_to(c, L::kBars, L::bEmpty + ring.st);
+        for (int k = 0; k < kKvSets; ++k) ring.next();
     }
-    drain(c, c.bar(L::kBars, L::bDrain));
+    drain(c, c.bar(L::kBars, L::bDrain + which));
 }
 
 // inter = A x^T, intra = z^T scores^T, and P = x y^T of the chunk after (kExact: of the chunk itself, since intra
-// takes P's columns)
+// takes P's only columns)
 template <int kMode>
 GDN_DEVICE void out_products_role(const Ctx& c) {
     using L = Layout<kMode>;
@@ -450,29 +492,29 @@ GDN_DEVICE void out_products_role(const Ctx& c) {
     constexpr uint32_t idPv = idesc_bf16(128, 64, true, false);
     const int32_t total = c.reps * c.chunks;
     const uint64_t dScores = sdesc_sw128(c.base + L::kScores, 16, 1024);
-    auto scores = [&](int st) {
+    auto scores = [&](int st, uint32_t set) {
         const uint64_t dx = k_major<kMode>(c, st, L::kX), dy = k_major<kMode>(c, st, L::kY);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-            mma_bf16(c.tmem + L::tP, dx + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4),
+            mma_bf16(c.tmem + L::tP + set, dx + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4),
                      dy + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), idKK, kk > 0);
         commit_to(c, L::kBars, L::bPFull);
     };
     Ring<L::kStages> ring;
-    uint32_t odd = 0;
     // kOut: the extra first turn issues chunk 0's scores
 #pragma unroll 1
     for (int32_t it = kMode == kOut ? -1 : 0; it < total; ++it) {
+        const uint32_t set = L::kPSets == 2 ? (it & 1) * 64 : 0;
         if (it >= 0) {
             const int st = ring.st;
             if (kMode == kExact && !c.wait(L::kBars, L::bFull + st, ring.phase)) break;
             // inter and intra have been read for the chunk before
-            if (it > 0 && !c.wait(L::kBars, L::bOFree, odd ^ 1u)) break;
+            if (it > 0 && !c.wait(L::kBars, L::bOFree, it - 1)) break;
             if (kMode == kExact) {
                 tc_fence_after();
-                scores(st);
+                scores(st, 0);
             }
-            if (!c.wait(L::kBars, L::bAReady, odd)) break;
+            if (!c.wait(L::kBars, L::bAReady, it)) break;
             tc_fence_after();
             const uint64_t dx = k_major<kMode>(c, st, L::kX);
 #pragma unroll
@@ -481,24 +523,24 @@ GDN_DEVICE void out_products_role(const Ctx& c) {
                 for (int kk = 0; kk < 8; ++kk)
                     mma_bf16_ta(c.tmem + L::tInter, c.tmem + L::tA + part * 64 + kk * 8,
                                 dx + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4), idKK, part < L::kParts - 1 || kk > 0);
-            if (!c.wait(L::kBars, L::bPReady, odd)) break;
+            if (!c.wait(L::kBars, L::bPReady, it)) break;
             tc_fence_after();
             const uint64_t dz = mn_major<kMode>(c, st, L::kZ);
 #pragma unroll
             for (int part = L::kParts - 1; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16(c.tmem + L::tIntra, dz + kk * 128, dScores + part * (kPanel >> 4) + kk * 2, idPv,
+                    mma_bf16(c.tmem + L::tP + set, dz + kk * 128, dScores + part * (kPanel >> 4) + kk * 2, idPv,
                              part < L::kParts - 1 || kk > 0);
             commit_to(c, L::kBars, L::bOFull);
             commit_to(c, L::kBars, L::bEmpty + st);
             ring.next();
-            odd ^= 1u;
         }
         if (kMode == kOut && it + 1 < total) {
+            // (the other set was read for the chunk before, whose release has been waited for above)
             if (!c.wait(L::kBars, L::bFull + ring.st, ring.phase)) break;
             tc_fence_after();
-            scores(ring.st);
+            scores(ring.st, set ^ 64u);
         }
     }
     drain(c, c.bar(L::kBars, L::bDrain + 1));
@@ -520,7 +562,7 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
     const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const int32_t total = c.reps * c.chunks;
-    uint32_t zeroed = 0, odd = 0;
+    uint32_t zeroed = 0;
     Ring<L::kStages> ring;
     // This warp's z indices 32 quad .. + 32 as four 8 x 8 matrices (8 tokens each way) per ldmatrix: matrix m of
     // 16 tokens is tokens 8 (m >> 1), z indices 8 (m & 1) (+ 16 for the second half); lane l gives row l % 8 of
@@ -530,7 +572,7 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
     const uint32_t at = L::kZ + (z >> 6) * kPanel + sw128_off(row, (z & 63) >> 3);
     const uint32_t at2 = L::kZ + (z >> 6) * kPanel + sw128_off(row, ((z + 16) & 63) >> 3);
 #pragma unroll 1
-    for (int32_t it = 0; it < total; ++it, ring.next(), odd ^= 1u) {
+    for (int32_t it = 0; it < total; ++it, ring.next()) {
         const int st = ring.st;
         if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
         const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
@@ -552,9 +594,10 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
 #pragma unroll 1
         for (int s = first; s < L::kSlots; s += stride) {
             // (a barrier's phase before its first completes at once)
-            if (!c.wait(L::kBars, L::bWFree + (s & 1), (L::kSlots == 2 ? odd : (uint32_t)(s >> 1)) ^ 1u)) return;
+            const uint32_t use = it * L::kSlots + s, buf = use % L::kSlotBufs;
+            if (!c.wait(L::kBars, L::bWFree + buf, use / L::kSlotBufs + 1)) return;
             tc_fence_after();
-            const uint32_t dst = c.tmem + lanes + L::tW + (s & 1) * L::kSlotCols;
+            const uint32_t dst = c.tmem + lanes + L::tW + buf * L::kSlotCols;
 #pragma unroll 1
             for (int t = s * L::kSlot; t < (s + 1) * L::kSlot; t += 16) {
                 // tokens t + 8 j + 2 (lane % 4) and the next
@@ -580,7 +623,7 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bWFull + (s & 1)));
+            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bWFull + buf));
         }
     }
 }
@@ -624,7 +667,7 @@ GDN_DEVICE void score_role(const Ctx& c) {
 #pragma unroll 1
         for (int s = first; s < first + (two ? 32 : 16); s += 16) {
             float p[16];
-            tmem_ld16w(c.tmem + lanes + L::tP + s, p);
+            tmem_ld16w(c.tmem + lanes + L::tP + (L::kPSets == 2 ? (it & 1) * 64 : 0) + s, p);
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
                 const float4 sh = *reinterpret_cast<const float4*>(gate + 128 + s + j);
@@ -726,7 +769,8 @@ GDN_DEVICE void state_role(const Ctx& c) {
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     float S[64];
     Ring<L::kStages> ring;
-    uint32_t odd = 0;                           // parity of the chunk
+    constexpr int kKvSets = L::kKvSets;
+    uint32_t it = 0;
     for (int r = 0; r < c.reps; ++r) {
         const int h = c.head0 + r;
         const int64_t own = ((int64_t)c.part.seq * p.Hv + h) * (kD * kD);
@@ -741,14 +785,15 @@ GDN_DEVICE void state_role(const Ctx& c) {
                 const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + ring.st * L::kGateBytes);
                 if (!c.wait(L::kBars, L::bFull + ring.st, ring.phase)) return;
                 const float2 gamma2 = make_float2(gate[256], gate[256]);
-                if (!c.wait(L::kBars, L::bKvFull, odd)) return;
+                if (!c.template wait_set<kKvSets>(L::kBars, L::bKvFull, it)) return;
                 tc_fence_after();
+                const uint32_t set = kKvSets == 2 ? it & 1u : 0u;
 #pragma unroll
-                for (int j = 0; j < 64; j += 16) {
-                    float kv[16];
-                    tmem_ld16w(c.tmem + lanes + L::tKv + half * 64 + j, kv);
+                for (int j = 0; j < 64; j += 32) {
+                    float kv[32];
+                    tmem_ld32w(c.tmem + lanes + L::tKv + set * 128 + half * 64 + j, kv);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
+                    for (int e = 0; e < 32; e += 2) {
                         const float2 x = fma2(gamma2, make_float2(S[j + e], S[j + e + 1]), make_float2(kv[e], kv[e + 1]));
                         S[j + e] = x.x;
                         S[j + e + 1] = x.y;
@@ -757,13 +802,13 @@ GDN_DEVICE void state_role(const Ctx& c) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(c.bar(L::kBars, L::bKvFree));
+                    mbar_arrive(c.bar(L::kBars, L::bKvFree + set));
                     mbar_arrive(c.bar(L::kBars, L::bEmpty + ring.st));
                 }
                 ring.next();
                 // inter has read the copy for the chunk before
-                if (L::kOuts && !c.wait(L::kBars, L::bOFull, odd)) return;
-                odd ^= 1u;
+                if (L::kOuts && !c.wait(L::kBars, L::bOFull, it)) return;
+                ++it;
             }
             if (L::kOuts && n < c.chunks) put_state<kMode>(c, lanes, half, S);
         }
@@ -786,7 +831,7 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
     const bool f32 = p.out_rep > 1 || !p.out_bf16;
     const uint32_t rows = L::kHalf * half;      // of a stage: where the output is staged, over x, whose products are done
     Ring<L::kStages> ring;
-    uint32_t odd = 0;                           // parity of the chunk
+    uint32_t it = 0;
     int held = -1;                              // the stage whose rows are leaving
     for (int r = 0; r < c.reps; ++r) {
 #pragma unroll 1
@@ -796,7 +841,8 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
             if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
             const int64_t t0 = c.chunk_start(n);
             const int valid = reinterpret_cast<const int32_t*>(gate)[257];
-            if (!c.wait(L::kBars, L::bOFull, odd)) return;
+            if (!c.wait(L::kBars, L::bOFull, it)) return;
+            const uint32_t set = L::kPSets == 2 ? it & 1u : 0u;
             tc_fence_after();
             if (held >= 0 && lane == 0) {       // the chunk before's rows have left its stage
                 bulk_wait_read();
@@ -818,7 +864,7 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                 for (int hz = 0; hz < 32; hz += 16) {
                     float inter[8], out[8];
                     const uint32_t src = c.tmem + lanes + ((uint32_t)hz << 16) + half * 32 + tb;
-                    tmem_ld_frag16x2w(src + L::tInter, src + L::tIntra, inter, out);
+                    tmem_ld_frag16x2w(src + L::tInter, src + L::tP + set * 64, inter, out);
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
                         const float2 x = fma2(e < 4 ? a0 : a1, make_float2(inter[e], inter[e + 1]),
@@ -865,7 +911,7 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                     k2 += __shfl_xor_sync(0xffffffffu, g2, 8);
                     k2 += __shfl_xor_sync(0xffffffffu, k2, 16);
                     if (lane < 16)
-                        reinterpret_cast<float*>(c.sm + L::kDots)[odd * 256 + warp * 32 + tb + (lane & 4) * 2 +
+                        reinterpret_cast<float*>(c.sm + L::kDots)[(it & 1u) * 256 + warp * 32 + tb + (lane & 4) * 2 +
                                                                   2 * (lane & 3) + (lane >> 3)] = k2;
                 }
             }
@@ -878,9 +924,8 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                 mbar_arrive(c.bar(L::kBars, L::bRows + half));
                 if (whole && quad != 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
             }
-            const uint32_t now = odd;
+            const uint32_t now = it++;
             ring.next();
-            odd ^= 1u;
             if (whole && quad != 0) continue;
             // the four warps of this half have their z indices in place
             if (!c.wait(L::kBars, L::bRows + half, now)) return;
@@ -928,7 +973,7 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
             if (kMode == kExact && quad == 0 && half * 32 + lane < valid) {
                 // (two buffers: the chunk after the next needs this stage, which this warp has not yet released)
                 static_assert(kMode != kExact || L::kStages == 2, "the buffers of the dot products");
-                const float* d = reinterpret_cast<const float*>(c.sm + L::kDots) + now * 256 + half * 128 + lane;
+                const float* d = reinterpret_cast<const float*>(c.sm + L::kDots) + (now & 1u) * 256 + half * 128 + lane;
                 p.dots[(int64_t)(c.head0 + r) * p.T + t0 + half * 32 + lane] = (d[0] + d[32]) + (d[64] + d[96]);
             }
             __syncwarp();
@@ -964,13 +1009,15 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         init(L::bPFull, 1);
         init(L::bPReady, 4);
         init(L::bAReady, 8);
-        init(L::bKvFull, 1);
-        init(L::bKvFree, 8);
+        for (int k = 0; k < 2; ++k) {
+            init(L::bKvFull + k, 1);
+            init(L::bKvFree + k, 8);
+        }
         init(L::bOFull, 1);
         init(L::bOFree, 8);
-        for (int s = 0; s < 2; ++s) {
-            init(L::bWFull + s, 4);
-            init(L::bWFree + s, 1);
+        for (int k = 0; k < L::kSlotBufs; ++k) {
+            init(L::bWFull + k, 4);
+            init(L::bWFree + k, 1);
         }
         init(L::bZeroed, kMode == kState ? 8 : 4);
         init(L::bRows, 4);
@@ -995,6 +1042,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     } else if (warp < 16) {
         regs_dec<kRegsOut>();
         if (L::kOuts) out_role<kMode>(c, &mo);
+        else if (warp == 8) decay_role<kMode>(c, 1, 2);
         bulk_wait();                            // rows still leaving (a role that gave up)
     } else if (warp < 20) {
         weight_role<kMode>(c, 0, kMode == kState ? 2 : 1);
@@ -1005,21 +1053,11 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     } else {
         regs_dec<kRegsRest>();
         if (warp == 24) load_role<kMode>(c, &mx, &my, &mz, &mu);
-        if (warp == 25) kv_role<kMode>(c);
+        if (warp == 25) kv_role<kMode>(c, 0);
         if (warp == 26 && L::kOuts) out_products_role<kMode>(c);
-        if (warp == 26 && kMode == kState) {
-            // the part's whole decay
-            double sum = 0.0;
-            for (int64_t t = part.t0 + (threadIdx.x & 31); t < part.t1; t += 32) {
-                const float g = w.p.g[t * w.p.ldg + head];
-                sum += g < kLinMinLogDecay ? kLinMinLogDecay : g;
-            }
-#pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            if ((threadIdx.x & 31) == 0) w.joint_decay[(int64_t)index * w.p.Hv + head] = (float)exp(sum);
-        }
+        if (warp == 26 && kMode == kState) kv_role<kMode>(c, 1);
         if (warp == 27) {
-            decay_role<kMode>(c);
+            decay_role<kMode>(c, 0, kMode == kState ? 2 : 1);
             mbar_wait(c.bar(L::kBars, L::bDone), 0, c.abort, kWaitLimitNs);
         }
     }
@@ -1031,6 +1069,13 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     if (*abort && threadIdx.x == 0) *w.err = 1u;
+    if (kMode == kState && threadIdx.x == 0) {
+        // the part's whole decay
+        const long long* sum = reinterpret_cast<const long long*>(sm + L::kMisc + 16);
+        const float* bad = reinterpret_cast<const float*>(sm + L::kMisc + 32);
+        w.joint_decay[(int64_t)index * w.p.Hv + head] =
+            exp2f((float)((double)(sum[0] + sum[1]) * (1.0 / 4294967296.0))) + bad[0] + bad[1];
+    }
     if (warp == 25) tmem_dealloc(tmem, 512);
 }
 
