@@ -15,31 +15,36 @@ constexpr int kSms = 148;
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // ---- parts --------------------------------------------------------------------------------------------
-// The length of a part, from what the host knows (T tokens in n_seq sequences, of which it assumes equal
-// lengths): the least of
-//     walk:  rounds of `heads` CTAs per part over the SMs, each reps * chunks * kWalk + kStart long
-//     states, where a sequence has several parts:  the same over all parts but the last, chunks * kState,
-//            and the scan
+// The length of a part, from what the host knows: T tokens in n_seq sequences, of which it assumes equal lengths
+// where it cuts them and any lengths where it leaves them whole.  The least of
+//     walk:    rounds of `heads` CTAs per part over the SMs, each reps * chunks * kWalk + kStart long
+//     states:  where a sequence has several parts, the same over all parts but the last, chunks * kStateStep long,
+//              and the scan
 // in microseconds, measured on B200.  Sequences that turn out longer than a part are cut.
 int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, int64_t most) {
-    constexpr double kWalk = 0.9, kStateStep = 0.5, kStart = 5.0, kScan = 6.0;
-    const int64_t chunks = (T + n_seq - 1) / n_seq / kC + 1;
-    double best = 0.0;
-    int64_t len = chunks;
+    constexpr double kWalk = 2.1, kStateStep = 0.85, kStart = 5.0, kScan = 8.0;
+    const int64_t all = (T + kC - 1) / kC, chunks = (T + n_seq - 1) / n_seq / kC + 1;
+    auto rounds = [](int64_t ctas) { return (double)((ctas + kSms - 1) / kSms); };
+    // no cuts: one round more than full ones can be as long as all tokens in one sequence
+    double best = -1.0;
+    int64_t len = most / kC;
+    if (T <= most) {
+        best = rounds((int64_t)n_seq * heads) * kStart + (rounds((int64_t)n_seq * heads) - 1) * (double)(chunks * reps) * kWalk +
+               (double)(all * reps) * kWalk;
+        len = all > 0 ? all : 1;
+    }
     for (int64_t parts = 1; parts <= chunks && parts <= kSms; ++parts) {
         const int64_t l = (chunks + parts - 1) / parts;
-        if (l * kC > most) continue;
+        if (l * kC > most || l >= all) continue;
         const int64_t n = (chunks + l - 1) / l;
-        auto rounds = [&](int64_t ctas) { return (double)((ctas + kSms - 1) / kSms); };
         double cost = rounds((int64_t)n_seq * n * heads) * ((double)(l * reps) * kWalk + kStart);
-        if (n > 1)
-            cost += rounds((int64_t)n_seq * (n - 1) * heads * reps) * ((double)l * kStateStep + kStart) + kScan;
-        if (best == 0.0 || cost < best) {
+        // (uneven sequences are cut even where their mean is not)
+        cost += rounds((int64_t)n_seq * (n > 1 ? n - 1 : 1) * heads * reps) * ((double)l * kStateStep + kStart) + kScan;
+        if (best < 0.0 || cost < best) {
             best = cost;
-            len = n == 1 && n_seq > 1 ? 2 * l : l;         // uneven sequences: up to twice the mean stay whole
+            len = n == 1 && 2 * l * kC <= most ? 2 * l : l;        // up to twice the mean stays whole
         }
     }
-    if (len * kC > most) len = most / kC;
     return (int32_t)(len * kC);
 }
 

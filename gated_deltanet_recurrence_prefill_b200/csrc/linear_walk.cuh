@@ -95,15 +95,15 @@ struct Part {
 GDN_DEVICE Part find_part(const Walk& w, int32_t index) {
     const int lane = threadIdx.x & 31;
     Part r{0, 0, -1, 0, 0, 0};
-    int64_t before = 0;
+    const uint32_t len = (uint32_t)w.part_len;
+    int32_t before = 0;
     for (int32_t i0 = 0; i0 < w.p.n_seq; i0 += 32) {
         const int32_t i = i0 + lane;
-        int64_t a = 0, b = 0;
-        int32_t n = 0;
+        int32_t a = 0, b = 0, n = 0;
         if (i < w.p.n_seq) {
             a = w.p.cu ? w.p.cu[i] : 0;
-            b = w.p.cu ? w.p.cu[i + 1] : w.p.T;
-            n = b > a ? (int32_t)((b - a + w.part_len - 1) / w.part_len) : 1;
+            b = w.p.cu ? w.p.cu[i + 1] : (int32_t)w.p.T;
+            n = b > a ? (int32_t)(((uint32_t)(b - a) + len - 1u) / len) : 1;
         }
         int32_t upto = n;
 #pragma unroll
@@ -111,24 +111,18 @@ GDN_DEVICE Part find_part(const Walk& w, int32_t index) {
             const int32_t x = __shfl_up_sync(0xffffffffu, upto, m);
             if (lane >= m) upto += x;
         }
-        const int32_t k = (int32_t)(index - before) - (upto - n);        // the part's number in this lane's sequence
+        const int32_t k = index - before - (upto - n);                   // the part's number in this lane's sequence
         const unsigned found = __ballot_sync(0xffffffffu, k >= 0 && k < n);
         if (found) {
             const int src = __ffs(found) - 1;
-            if (lane == src) {
-                r.t0 = a + (int64_t)k * w.part_len;
-                r.t1 = r.t0 + w.part_len < b ? r.t0 + w.part_len : b;
-                r.seq = i;
-                r.first = w.p.backward ? k == n - 1 : k == 0;
-                r.last = w.p.backward ? k == 0 : k == n - 1;
-                r.alone = n == 1;
-            }
-            r.t0 = __shfl_sync(0xffffffffu, r.t0, src);
-            r.t1 = __shfl_sync(0xffffffffu, r.t1, src);
-            r.seq = __shfl_sync(0xffffffffu, r.seq, src);
-            r.first = __shfl_sync(0xffffffffu, r.first, src);
-            r.last = __shfl_sync(0xffffffffu, r.last, src);
-            r.alone = __shfl_sync(0xffffffffu, r.alone, src);
+            const int32_t s0 = __shfl_sync(0xffffffffu, a, src), s1 = __shfl_sync(0xffffffffu, b, src);
+            const int32_t kk = __shfl_sync(0xffffffffu, k, src), nn = __shfl_sync(0xffffffffu, n, src);
+            r.t0 = s0 + (int64_t)kk * len;
+            r.t1 = r.t0 + len < s1 ? r.t0 + len : s1;
+            r.seq = i0 + src;
+            r.first = w.p.backward ? kk == nn - 1 : kk == 0;
+            r.last = w.p.backward ? kk == 0 : kk == nn - 1;
+            r.alone = nn == 1;
             return r;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
@@ -172,7 +166,8 @@ struct Layout {
     static constexpr int bFull = 0, bEmpty = bFull + kStages, bPFull = bEmpty + kStages, bPReady = bPFull + 1,
                          bAReady = bPReady + 1, bKvFull = bAReady + 1, bKvFree = bKvFull + 2, bOFull = bKvFree + 2,
                          bOFree = bOFull + 1, bWFull = bOFree + 1, bWFree = bWFull + kSlotBufs, bZeroed = bWFree + kSlotBufs,
-                         bRows = bZeroed + 1, bDrain = bRows + 2, bDone = bDrain + 2, kBarCount = bDone + 1;
+                         bRows = bZeroed + 1, bDrain = bRows + 2, bDone = bDrain + 2, bStateIn = bDone + 1,
+                         kBarCount = bStateIn + 1;
     static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag, a part's decay
     static constexpr uint32_t kSmem = kMisc + 64;
     static constexpr uint32_t kAlloc = kSmem + 1024;
@@ -291,6 +286,8 @@ GDN_DEVICE void load_role(const Ctx& c, const CUtensorMap* mx, const CUtensorMap
 #pragma unroll 1
         for (int32_t n = 0; n < c.chunks; ++n, ++it, t += step, ring.next()) {
             if (it >= L::kStages && !c.wait(L::kBars, L::bEmpty + ring.st, ring.phase ^ 1u)) goto out;
+            // the starting state comes in through the last stage
+            if (kMode == kOut && it == L::kStages - 1 && !c.wait(L::kBars, L::bStateIn, 0)) goto out;
             const uint32_t full = c.bar(L::kBars, L::bFull + ring.st), s = c.base + ring.st * L::kStage;
             mbar_arrive_expect_tx(full, L::kStage);
 #pragma unroll 1
@@ -733,30 +730,64 @@ GDN_DEVICE void put_state(const Ctx& c, uint32_t lanes, int half, const float* S
     if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar(L::kBars, L::bAReady));
 }
 
-GDN_DEVICE void load_state(float* S, const float* src, bool transposed, int z, int half) {
+// A thread's 64 columns of a row, to and from a state in memory.  Transposed, lanes are neighbours there.  As it is,
+// they are a row apart, and a warp's block of 32 rows x 64 columns goes through 8 KB of shared memory (16-byte pieces
+// swizzled by the row) so that memory sees 256 bytes at a time; without room for that, row by row (6,000 cycles
+// more for a state).
+GDN_DEVICE float4* state_piece(uint8_t* buf, int row, int piece) {
+    return reinterpret_cast<float4*>(buf + row * 256 + ((piece ^ (row & 15)) << 4));
+}
+
+GDN_DEVICE void load_state(float* S, const float* src, bool transposed, int z, int half, uint8_t* buf) {
+    const int lane = threadIdx.x & 31;
     if (!src) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) S[j] = 0.f;
-    } else if (transposed) {
+        return;
+    }
+    if (transposed) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) S[j] = src[(half * 64 + j) * kD + z];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src + z * kD + half * 64 + j);
-            S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+        return;
+    }
+    if (buf) {
+        const float* block = src + (z - lane) * kD + half * 64;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            const int row = 2 * i + (lane >> 4);
+            *state_piece(buf, row, lane & 15) = *reinterpret_cast<const float4*>(block + row * kD + (lane & 15) * 4);
         }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < 64; j += 4) {
+        const float4 v = buf ? *state_piece(buf, lane, j / 4) : *reinterpret_cast<const float4*>(src + z * kD + half * 64 + j);
+        S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
     }
 }
 
-GDN_DEVICE void store_state(const float* S, float* dst, bool transposed, int z, int half) {
+GDN_DEVICE void store_state(const float* S, float* dst, bool transposed, int z, int half, uint8_t* buf) {
+    const int lane = threadIdx.x & 31;
     if (transposed) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) dst[(half * 64 + j) * kD + z] = S[j];
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int j = 0; j < 64; j += 4)
-            *reinterpret_cast<float4*>(dst + z * kD + half * 64 + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+    for (int j = 0; j < 64; j += 4) {
+        const float4 v = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        if (buf) *state_piece(buf, lane, j / 4) = v;
+        else *reinterpret_cast<float4*>(dst + z * kD + half * 64 + j) = v;
+    }
+    if (buf) {
+        __syncwarp();
+        float* block = dst + (z - lane) * kD + half * 64;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            const int row = 2 * i + (lane >> 4);
+            *reinterpret_cast<float4*>(block + row * kD + (lane & 15) * 4) = *state_piece(buf, row, lane & 15);
+        }
+        __syncwarp();
     }
 }
 
@@ -775,9 +806,15 @@ GDN_DEVICE void state_role(const Ctx& c) {
         const int h = c.head0 + r;
         const int64_t own = ((int64_t)c.part.seq * p.Hv + h) * (kD * kD);
         const int64_t joint = ((int64_t)c.index * p.Hv + h) * (kD * kD);
-        if (kMode == kState) load_state(S, nullptr, false, z, half);
-        else if (c.w.split && !c.part.alone) load_state(S, c.w.joint + joint, c.w.joint_t != 0, z, half);
-        else load_state(S, p.init ? p.init + own : nullptr, p.state_t != 0, z, half);
+        // kOut: the last stage, which the loads leave alone until then
+        uint8_t* room = kMode == kOut && r == 0 ? c.sm + (L::kStages - 1) * L::kStage + warp * 8192 : nullptr;
+        if (kMode == kState) load_state(S, nullptr, false, z, half, nullptr);
+        else if (c.w.split && !c.part.alone) load_state(S, c.w.joint + joint, c.w.joint_t != 0, z, half, room);
+        else load_state(S, p.init ? p.init + own : nullptr, p.state_t != 0, z, half, room);
+        if (kMode == kOut && r == 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bStateIn));
+        }
         // turn n: the state behind chunk n - 1, and its copy for chunk n
 #pragma unroll 1
         for (int32_t n = 0; n <= c.chunks; ++n) {
@@ -812,8 +849,12 @@ GDN_DEVICE void state_role(const Ctx& c) {
             }
             if (L::kOuts && n < c.chunks) put_state<kMode>(c, lanes, half, S);
         }
-        if (kMode == kState) store_state(S, c.w.joint + joint, false, z, half);
-        else if (p.fin && c.part.last) store_state(S, p.fin + own, p.state_t != 0, z, half);
+        // After the last head's last chunk nothing is loaded any more.  kState: the products are done with every stage.
+        // kOut: and so is the output with the stage after the last chunk's, that of the third last chunk (its rows had
+        // left before the second last chunk's inter and intra were released, which the last chunk's products needed).
+        room = r + 1 == c.reps && kMode != kExact ? c.sm + (kMode == kOut ? ring.st * L::kStage : 0) + warp * 8192 : nullptr;
+        if (kMode == kState) store_state(S, c.w.joint + joint, false, z, half, room);
+        else if (p.fin && c.part.last) store_state(S, p.fin + own, p.state_t != 0, z, half, room);
     }
 }
 
@@ -1025,6 +1066,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         init(L::bDrain, 1);
         init(L::bDrain + 1, 1);
         init(L::bDone, 27);
+        init(L::bStateIn, 8);
         *abort = 0;
         fence_mbar_init();
     }
