@@ -634,46 +634,63 @@ def _backward(entry, q, k, v, a, b, A_log, dt_bias, d_o, d_final_state, cu_seqle
 
 class _Launch:
     """The device and stream a call runs on: the device of its tensors (which must share one), made current for
-    the call, and `stream` or that device's current stream, which allocations of the call then belong to."""
+    the call, and `stream` or that device's current stream, which allocations of the call then belong to.  With
+    neither to be changed, entering it costs one look-up of the current stream."""
+
+    __slots__ = ("device", "scopes")
 
     def __init__(self, stream, *tensors):
         import torch
-        self.device = None
+        index = -1
         for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("all tensors must be CUDA tensors")
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError(f"all tensors must be on one device, got {self.device} and {t.device}")
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-        self.scopes = []
-        if self.device.index != torch.cuda.current_device():
-            self.scopes.append(torch.cuda.device(self.device))
+            if t is not None:
+                i = t.get_device()
+                if i < 0:
+                    raise ValueError("all tensors must be CUDA tensors")
+                if index < 0:
+                    index = i
+                elif i != index:
+                    raise ValueError(f"all tensors must be on one device, got cuda:{index} and cuda:{i}")
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        self.device, self.scopes = index, None
+        if index != torch.cuda.current_device():
+            self.scopes = [torch.cuda.device(index)]
         if stream is not None:
-            self.scopes.append(torch.cuda.stream(stream))
+            self.scopes = (self.scopes or []) + [torch.cuda.stream(stream)]
 
     def __enter__(self):
         import torch
-        for s in self.scopes:
-            s.__enter__()
-        return C.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+        if self.scopes is not None:
+            for s in self.scopes:
+                s.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device)
 
     def __exit__(self, *e):
-        for s in reversed(self.scopes):
-            s.__exit__(*e)
+        if self.scopes is not None:
+            for s in reversed(self.scopes):
+                s.__exit__(*e)
+
+
+def _at(t):
+    """The address of a tensor, NULL for None (as _ptr, without an object for each)."""
+    return None if t is None else t.data_ptr()
+
+
+def _want(t, dtype, shape, name):
+    """_need for a tensor whose device is checked elsewhere: one comparison each where all is well."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, shape, name, device=None)
+    return t
 
 
 def _token_rows(t, T, H, d, name):
     """Checks a bf16 [T, H, d] tensor whose tokens may be any multiple of 8 elements apart (a view of a packed
     projection); returns that distance, 0 for a dense tensor."""
     import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (T, H, d):
+    if t.shape != (T, H, d):
         raise ValueError(f"{name}: expected shape {(T, H, d)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return 0
@@ -693,9 +710,9 @@ def _linear_shapes(q, k, v, g, cu_seqlens):
     lds = (_token_rows(q, T, Hqk, d, "q"), _token_rows(k, T, Hqk, d, "k"), _token_rows(v, T, Hv, d, "v"))
     if g.dim() not in (1, 2):
         raise ValueError(f"g: expected shape {(T, Hv)} or {(Hv,)}, got {tuple(g.shape)}")
-    _need(g, torch.float32, (T, Hv) if g.dim() == 2 else (Hv,), "g")
+    _want(g, torch.float32, (T, Hv) if g.dim() == 2 else (Hv,), "g")
     if cu_seqlens is not None:
-        _need(cu_seqlens, torch.int32, (n_seq + 1,), "cu_seqlens")
+        _want(cu_seqlens, torch.int32, (n_seq + 1,), "cu_seqlens")
     return T, Hqk, Hv, d, n_seq, lds
 
 
@@ -704,7 +721,7 @@ def _given(t, dtype, shape, name, device):
     import torch
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    return _need(t, dtype, shape, name)
+    return _want(t, dtype, shape, name)
 
 
 def _workspace(workspace, size, device):
@@ -734,7 +751,7 @@ def linear_prefill(q, k, v, g, cu_seqlens=None, scale=None, initial_state=None, 
     if o_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("o must be float32 or bfloat16")
     if initial_state is not None:
-        _need(initial_state, torch.float32, (n_seq, Hv, d, d), "initial_state")
+        _want(initial_state, torch.float32, (n_seq, Hv, d, d), "initial_state")
     if scale is None:
         scale = d ** -0.5
     with _Launch(stream, q, k, v, g, cu_seqlens, initial_state, final_state, o, workspace) as s:
@@ -743,9 +760,9 @@ def linear_prefill(q, k, v, g, cu_seqlens=None, scale=None, initial_state=None, 
         if final_state is not None or want_final_state:
             final_state = _given(final_state, torch.float32, (n_seq, Hv, d, d), "final_state", dev)
         ws, ws_bytes = _workspace(workspace, lib().gdn_linear_prefill_workspace_size(n_seq, T, Hqk, Hv, d), dev)
-        st = lib().gdn_linear_prefill(_ptr(q), _ptr(k), _ptr(v), *lds, _ptr(g), g.dim() - 1, _ptr(cu_seqlens), n_seq,
-                                      T, Hqk, Hv, d, float(scale), _ptr(initial_state), _ptr(final_state), _ptr(o),
-                                      int(o_dtype == torch.bfloat16), _ptr(ws), ws_bytes, s)
+        st = lib().gdn_linear_prefill(_at(q), _at(k), _at(v), *lds, _at(g), g.dim() - 1, _at(cu_seqlens), n_seq,
+                                      T, Hqk, Hv, d, float(scale), _at(initial_state), _at(final_state), _at(o),
+                                      int(o_dtype == torch.bfloat16), _at(ws), ws_bytes, s)
     _check("gdn_linear_prefill", st)
     return o, final_state
 
@@ -763,10 +780,10 @@ def linear_prefill_backward(q, k, v, g, d_o, d_final_state=None, cu_seqlens=None
         grad_dtype = next((given[n].dtype for n in ("dq", "dk", "dv") if given.get(n) is not None), torch.bfloat16)
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("the gradients must be float32 or bfloat16")
-    _need(d_o, torch.bfloat16, (T, Hv, d), "d_o")
+    _want(d_o, torch.bfloat16, (T, Hv, d), "d_o")
     for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
         if t is not None:
-            _need(t, torch.float32, (n_seq, Hv, d, d), name)
+            _want(t, torch.float32, (n_seq, Hv, d, d), name)
     if scale is None:
         scale = d ** -0.5
     with _Launch(stream, q, k, v, g, d_o, cu_seqlens, initial_state, d_final_state, workspace, *given.values()) as s:
@@ -779,10 +796,10 @@ def linear_prefill_backward(q, k, v, g, d_o, d_final_state=None, cu_seqlens=None
         size = lib().gdn_linear_prefill_backward_workspace_size(n_seq, T, Hqk, Hv, d)
         ws, ws_bytes = _workspace(workspace, size, dev)
         st = lib().gdn_linear_prefill_backward(
-            _ptr(q), _ptr(k), _ptr(v), *lds, _ptr(g), g.dim() - 1, _ptr(cu_seqlens), n_seq, T, Hqk, Hv, d,
-            float(scale), _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(out["dq"]), _ptr(out["dk"]),
-            _ptr(out["dv"]), int(grad_dtype == torch.bfloat16), _ptr(out["dg"]), _ptr(out["d_initial_state"]),
-            _ptr(ws), ws_bytes, s)
+            _at(q), _at(k), _at(v), *lds, _at(g), g.dim() - 1, _at(cu_seqlens), n_seq, T, Hqk, Hv, d,
+            float(scale), _at(initial_state), _at(d_o), _at(d_final_state), _at(out["dq"]), _at(out["dk"]),
+            _at(out["dv"]), int(grad_dtype == torch.bfloat16), _at(out["dg"]), _at(out["d_initial_state"]),
+            _at(ws), ws_bytes, s)
     _check("gdn_linear_prefill_backward", st)
     return out
 
@@ -797,16 +814,16 @@ def linear_decode_step(q, k, v, g, state, n_seq, layers, slot=None, scale=None, 
     Hv = v.shape[1]
     if U != n_seq * layers or layers <= 0:
         raise ValueError("q.shape[0] must equal n_seq * layers")
-    _need(q, torch.bfloat16, (U, Hqk, d), "q")
-    _need(k, torch.bfloat16, (U, Hqk, d), "k")
-    _need(v, torch.bfloat16, (U, Hv, d), "v")
+    _want(q, torch.bfloat16, (U, Hqk, d), "q")
+    _want(k, torch.bfloat16, (U, Hqk, d), "k")
+    _want(v, torch.bfloat16, (U, Hv, d), "v")
     per_unit = g.shape[0] != layers or n_seq == 1
-    _need(g, torch.float32, (U if per_unit else layers, Hv), "g")
+    _want(g, torch.float32, (U if per_unit else layers, Hv), "g")
     n_slots = state.shape[0] // layers
     bf16 = state.dtype == torch.bfloat16
-    _need(state, torch.bfloat16 if bf16 else torch.float32, (n_slots * layers, Hv, d, d), "state")
+    _want(state, torch.bfloat16 if bf16 else torch.float32, (n_slots * layers, Hv, d, d), "state")
     if slot is not None:
-        _need(slot, torch.int32, (n_seq,), "slot")
+        _want(slot, torch.int32, (n_seq,), "slot")
     if o_dtype is None:
         o_dtype = o.dtype if o is not None else torch.float32
     if o_dtype not in (torch.float32, torch.bfloat16):
@@ -815,8 +832,8 @@ def linear_decode_step(q, k, v, g, state, n_seq, layers, slot=None, scale=None, 
         scale = d ** -0.5
     with _Launch(stream, q, k, v, g, state, slot, o) as s:
         o = _given(o, o_dtype, (U, Hv, d), "o", q.device)
-        st = lib().gdn_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), int(per_unit), _ptr(slot), n_seq, layers,
-                                          Hqk, Hv, d, float(scale), n_slots, _ptr(state), int(bf16), _ptr(o),
+        st = lib().gdn_linear_decode_step(_at(q), _at(k), _at(v), _at(g), int(per_unit), _at(slot), n_seq, layers,
+                                          Hqk, Hv, d, float(scale), n_slots, _at(state), int(bf16), _at(o),
                                           int(o_dtype == torch.bfloat16), s)
     _check("gdn_linear_decode_step", st)
     return o
@@ -846,7 +863,7 @@ def _index(t, n, name):
     import torch
     if t.dim() != 1:
         raise ValueError(f"{name} must be one-dimensional")
-    return _need(t, torch.int32, (t.shape[0] if n is None else n,), name)
+    return _want(t, torch.int32, (t.shape[0] if n is None else n,), name)
 
 
 def state_copy(buffers, src, dst, stream=None):
@@ -858,7 +875,7 @@ def state_copy(buffers, src, dst, stream=None):
     n = src.shape[0]
     _index(dst, n, "dst")
     with _Launch(stream, src, dst, *tensors) as s:
-        st = lib().gdn_state_copy(array, nb, n_slots, _ptr(src), _ptr(dst), n, s)
+        st = lib().gdn_state_copy(array, nb, n_slots, _at(src), _at(dst), n, s)
     _check("gdn_state_copy", st)
 
 
@@ -877,7 +894,7 @@ def state_fork(buffers, live, src, dst=None, workspace=None, stream=None):
     with _Launch(stream, live, src, dst, workspace, *tensors) as s:
         dst = _given(dst, torch.int32, (n,), "dst", live.device)
         ws, ws_bytes = _state_workspace(workspace, n_slots, live.device)
-        st = lib().gdn_state_fork(array, nb, n_slots, _ptr(live), _ptr(src), _ptr(dst), n, _ptr(ws), ws_bytes, s)
+        st = lib().gdn_state_fork(array, nb, n_slots, _at(live), _at(src), _at(dst), n, _at(ws), ws_bytes, s)
     _check("gdn_state_fork", st)
     return dst
 
@@ -891,7 +908,7 @@ def state_compact(buffers, live, moved=None, workspace=None, stream=None):
     with _Launch(stream, live, moved, workspace, *tensors) as s:
         moved = _given(moved, torch.int32, (n_slots,), "moved", live.device)
         ws, ws_bytes = _state_workspace(workspace, n_slots, live.device)
-        st = lib().gdn_state_compact(array, nb, n_slots, _ptr(live), _ptr(moved), _ptr(ws), ws_bytes, s)
+        st = lib().gdn_state_compact(array, nb, n_slots, _at(live), _at(moved), _at(ws), ws_bytes, s)
     _check("gdn_state_compact", st)
     return moved
 
@@ -901,5 +918,5 @@ def state_free(live, slots, stream=None):
     _index(live, None, "live")
     _index(slots, None, "slots")
     with _Launch(stream, live, slots) as s:
-        st = lib().gdn_state_free(_ptr(live), live.shape[0], _ptr(slots), slots.shape[0], s)
+        st = lib().gdn_state_free(_at(live), live.shape[0], _at(slots), slots.shape[0], s)
     _check("gdn_state_free", st)

@@ -2,6 +2,8 @@
 // the prefill is one pass, its gradients are three (linear_attn.h).
 #include <cuda.h>
 
+#include <atomic>
+
 #include "linear_walk.cuh"
 
 namespace gdn {
@@ -247,6 +249,20 @@ bool make_out_map(CUtensorMap* m, const LinPass& p) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// raises a kernel's limit of dynamic shared memory, once per device (`done`: the devices where it has been)
+std::atomic<uint64_t> allowed[3];
+
+cudaError_t allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>& done) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <int kMode>
 cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
     CUtensorMap mx{}, my{}, mz{}, mu{}, mo{};
@@ -256,8 +272,7 @@ cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
         return cudaErrorInvalidValue;
     const int64_t blocks = (int64_t)w.n_parts * (kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(lin_walk_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Layout<kMode>::kAlloc);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(lin_walk_kernel<kMode>), Layout<kMode>::kAlloc, allowed[kMode]);
     if (e != cudaSuccess) return e;
     lin_walk_kernel<kMode><<<(unsigned)blocks, kThreads, Layout<kMode>::kAlloc, s>>>(mx, my, mz, mu, mo, w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
