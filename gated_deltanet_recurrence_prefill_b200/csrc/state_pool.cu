@@ -30,7 +30,7 @@ GDN_DEVICE void cp_async16(uint32_t dst, const void* src) {
 constexpr int kCopyThreads = 512;
 constexpr int kCopyStage = 48 * 1024;          // bytes of an item; a CTA has room for two, an SM for two CTAs
 constexpr int kCopyCtas = 2;
-constexpr int kCopyMinRange = 128;             // least bytes of a page in an item
+constexpr int kCopyMinRange = 64;              // least bytes of a page in an item (1,024 entries: 128 KB of room)
 
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas)
 state_copy_kernel(StateBuffers b, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int32_t n,
