@@ -105,7 +105,9 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_con
 // state and its gradient behind token t,
 //     dg_t = <S_end, dS_end> + sum_{t' >= t, same part} (r_t' - c_t'),
 // the first term at the part's end from the joints (or the final state), the sums in 64 bits from the last
-// token back.  One CTA per (part, head).
+// token back.  The sum at the part's first token is known too, <S, dS> in front of it: what the float32 errors of
+// r and c have added up to by then is taken back in proportion to the tokens summed, which leaves about 0.6 of the
+// error (a random walk tied down at both ends).  One CTA per (part, head).
 constexpr int kDgThreads = 256;
 
 GDN_DEVICE double block_sum(double x, double* sm) {
@@ -119,41 +121,60 @@ GDN_DEVICE double block_sum(double x, double* sm) {
     return s;
 }
 
+// <a, b> of two states, 0 if one is NULL
+GDN_DEVICE double state_product(const float* a, const float* b, double* sm) {
+    if (!a || !b) return 0.0;
+    double s = 0.0;
+    for (int i = threadIdx.x * 4; i < kD * kD; i += kDgThreads * 4) {
+        const float4 x = *reinterpret_cast<const float4*>(a + i), y = *reinterpret_cast<const float4*>(b + i);
+        s += ((double)x.x * y.x + (double)x.y * y.y) + ((double)x.z * y.z + (double)x.w * y.w);
+    }
+    return block_sum(s, sm);
+}
+
+struct DgArgs {
+    const float* r;
+    const float* c;
+    const float* joint_end;         // dS at the parts' ends
+    const float* fin;               // the final states and their gradients, or NULL
+    const float* d_fin;
+    const float* d_init;            // the initial states' gradients, or NULL (the states: Walk's init)
+    float* dg;
+    double* part_sum;               // for shared decays: the parts' sums instead of dg
+};
+
 __global__ void __launch_bounds__(kDgThreads)
-lin_dg_kernel(const __grid_constant__ Walk w, const float* r, const float* c, const float* joint_end, const float* fin,
-              const float* d_fin, float* dg, double* part_sum) {
+lin_dg_kernel(const __grid_constant__ Walk w, const __grid_constant__ DgArgs a) {
     __shared__ double sm[kDgThreads / 32];
     const int Hv = w.p.Hv;
     const int32_t index = blockIdx.x / Hv;
     const int h = blockIdx.x % Hv, tid = threadIdx.x;
     const Part part = find_part(w, index);
-    if (part.seq < 0) {
-        if (part_sum && tid == 0) part_sum[(int64_t)index * Hv + h] = 0.0;
+    if (part.seq < 0 || part.t1 == part.t0) {
+        if (a.part_sum && tid == 0) a.part_sum[(int64_t)index * Hv + h] = 0.0;
         return;
     }
-    const float *a = nullptr, *b = nullptr;
-    if (!part.last) {
-        a = w.joint + ((int64_t)(index + 1) * Hv + h) * (kD * kD);
-        b = joint_end + ((int64_t)index * Hv + h) * (kD * kD);
-    } else if (d_fin) {
-        a = fin + ((int64_t)part.seq * Hv + h) * (kD * kD);
-        b = d_fin + ((int64_t)part.seq * Hv + h) * (kD * kD);
-    }
-    double behind = 0.0;
-    if (a) {
-        for (int i = tid * 4; i < kD * kD; i += kDgThreads * 4) {
-            const float4 x = *reinterpret_cast<const float4*>(a + i), y = *reinterpret_cast<const float4*>(b + i);
-            behind += ((double)x.x * y.x + (double)x.y * y.y) + ((double)x.z * y.z + (double)x.w * y.w);
-        }
-        behind = block_sum(behind, sm);
+    auto state = [&](const float* base, int64_t i) { return base ? base + (i * Hv + h) * (kD * kD) : nullptr; };
+    double behind = part.last ? state_product(state(a.fin, part.seq), state(a.d_fin, part.seq), sm)
+                              : state_product(state(w.joint, index + 1), state(a.joint_end, index), sm);
+    const float* r = a.r + (int64_t)h * w.p.T;
+    const float* c = a.c + (int64_t)h * w.p.T;
+    double drift = 0.0;
+    if (!part.first || !w.p.init || a.d_init) {
+        double sum = 0.0;
+        for (int64_t t = part.t0 + tid; t < part.t1; t += kDgThreads) sum += (double)r[t] - (double)c[t];
+        sum = block_sum(sum, sm);
+        const double front = part.first ? state_product(state(w.p.init, part.seq), state(a.d_init, part.seq), sm)
+                                        : state_product(state(w.joint, index), state(a.joint_end, index - 1), sm);
+        drift = (behind + sum - front) / (double)(part.t1 - part.t0);
+        if (!(fabs(drift) <= 1e300)) drift = 0.0;          // a sequence with inf or NaN
     }
     double total = 0.0;
     for (int64_t end = part.t1; end > part.t0; end -= kDgThreads) {
         // thread 0 takes the last token of the block
         const int64_t t = end - 1 - tid;
         const bool there = t >= part.t0;
-        double x = there ? (double)r[(int64_t)h * w.p.T + t] - (double)c[(int64_t)h * w.p.T + t] : 0.0;
-        double upto = x;
+        double upto = there ? (double)r[t] - (double)c[t] : 0.0;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, upto, m);
@@ -168,15 +189,16 @@ lin_dg_kernel(const __grid_constant__ Walk w, const float* r, const float* c, co
         }
         __syncthreads();
         if (there) {
-            const double d = w.p.g[t * w.p.ldg + h] <= kLinMinLogDecay ? 0.0 : behind + upto;
-            if (!part_sum) dg[t * Hv + h] = (float)d;
+            const double d = w.p.g[t * w.p.ldg + h] <= kLinMinLogDecay
+                                 ? 0.0 : behind + upto - drift * (double)(part.t1 - t);
+            if (!a.part_sum) a.dg[t * Hv + h] = (float)d;
             total += d;
         }
         behind += all;
     }
-    if (part_sum) {
+    if (a.part_sum) {
         total = block_sum(total, sm);
-        if (tid == 0) part_sum[(int64_t)index * Hv + h] = total;
+        if (tid == 0) a.part_sum[(int64_t)index * Hv + h] = total;
     }
 }
 
@@ -422,8 +444,9 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     w.p.out = a.dv;
     if ((e = launch_walk<kOut>(w, s)) != cudaSuccess) return e;
     double* sums = a.ldg ? nullptr : reinterpret_cast<double*>(ws + b.sums);
-    lin_dg_kernel<<<(unsigned)(b.j.n_parts * a.Hv), kDgThreads, 0, s>>>(fwd, floats(b.qdq), floats(b.kdk), bwd.joint, fin,
-                                                                    a.d_final_state, a.dg, sums);
+    fwd.p.init = a.initial_state;
+    const DgArgs dg{floats(b.qdq), floats(b.kdk), bwd.joint, fin, a.d_final_state, a.d_initial_state, a.dg, sums};
+    lin_dg_kernel<<<(unsigned)(b.j.n_parts * a.Hv), kDgThreads, 0, s>>>(fwd, dg);
     if ((e = cudaGetLastError()) != cudaSuccess || a.ldg) return e;
     lin_dg_sum_kernel<<<a.Hv, 32, 0, s>>>(sums, b.j.n_parts, a.Hv, a.dg);
     return cudaGetLastError();
