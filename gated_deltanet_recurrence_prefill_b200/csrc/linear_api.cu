@@ -54,6 +54,9 @@ gdn_status check_buffers(const gdn_state_buffer* buffers, int32_t n_buffers, int
         if (buffers[i].slot_bytes > ((int64_t)1 << 38)) return GDN_ERR_UNSUPPORTED;
         b.data[i] = static_cast<uint8_t*>(buffers[i].data);
         b.bytes[i] = buffers[i].slot_bytes;
+        for (int k = 0; k < i; ++k)            // a buffer named twice would be moved twice
+            if (b.data[k] < b.data[i] + b.bytes[i] * n_slots && b.data[i] < b.data[k] + b.bytes[k] * n_slots)
+                return GDN_ERR_INVALID_ARG;
     }
     b.n = n_buffers;
     b.n_slots = n_slots;

@@ -18,7 +18,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // ---- parts --------------------------------------------------------------------------------------------
 // The length of a part, from what the host knows: T tokens in n_seq sequences, of which it assumes equal lengths
-// where it cuts them and any lengths where it leaves them whole.  The least of
+// where it cuts them, and one of eight times the mean where it leaves them whole.  The least of
 //     walk:    rounds of `heads` CTAs per part over the SMs, each reps * chunks * kWalk + kStart long
 //     states:  where a sequence has several parts, the same over all parts but the last, chunks * kStateStep long,
 //              and the scan
@@ -27,12 +27,11 @@ int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, i
     constexpr double kWalk = 2.1, kStateStep = 0.85, kStart = 5.0, kScan = 8.0;
     const int64_t all = (T + kC - 1) / kC, chunks = (T + n_seq - 1) / n_seq / kC + 1;
     auto rounds = [](int64_t ctas) { return (double)((ctas + kSms - 1) / kSms); };
-    // no cuts: one round more than full ones can be as long as all tokens in one sequence
     double best = -1.0;
     int64_t len = most / kC;
     if (T <= most) {
         best = rounds((int64_t)n_seq * heads) * kStart + (rounds((int64_t)n_seq * heads) - 1) * (double)(chunks * reps) * kWalk +
-               (double)(all * reps) * kWalk;
+               (double)((all < 8 * chunks ? all : 8 * chunks) * reps) * kWalk;
         len = all > 0 ? all : 1;
     }
     for (int64_t parts = 1; parts <= chunks && parts <= kSms; ++parts) {
@@ -55,25 +54,21 @@ int32_t part_count(int32_t n_seq, int64_t T, int32_t part_len) { return (int32_t
 // Turns each part's own sum into its starting state: start' = decay * start + own along the parts of a
 // sequence, in the pass's direction, from init.  One CTA per (sequence, head, 1024 elements).
 constexpr int kScanThreads = 256;
+constexpr int kScanSeqs = 32;                  // sequences at a time
 
-__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_constant__ Walk w) {
-    __shared__ int32_t before_sm[kScanThreads / 32];
-    const int seq = blockIdx.x / w.p.Hv, h = blockIdx.x % w.p.Hv;
-    auto parts = [&](int i) {
-        const int64_t a = w.p.cu ? w.p.cu[i] : 0, b = w.p.cu ? w.p.cu[i + 1] : w.p.T;
-        return b > a ? (int32_t)((b - a + w.part_len - 1) / w.part_len) : 1;
-    };
-    const int n = parts(seq);
+GDN_DEVICE void scan_sequence(const Walk& w, int seq, int h, int e) {
+    int32_t before = 0, n;
+    if (w.part_seq) {
+        before = w.seq_first[seq];
+        n = w.seq_first[seq + 1] - before;
+    } else {                                    // (at most 32 sequences)
+        auto parts = [&](int i) {
+            return parts_of(w, w.p.cu ? w.p.cu[i] : 0, w.p.cu ? w.p.cu[i + 1] : (int32_t)w.p.T);
+        };
+        n = parts(seq);
+        for (int i = 0; i < seq; ++i) before += parts(i);
+    }
     if (n == 1) return;
-    int32_t before = 0;
-    for (int i = threadIdx.x; i < seq; i += kScanThreads) before += parts(i);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) before += __shfl_xor_sync(0xffffffffu, before, m);
-    if ((threadIdx.x & 31) == 0) before_sm[threadIdx.x >> 5] = before;
-    __syncthreads();
-    before = 0;
-    for (int i = 0; i < kScanThreads / 32; ++i) before += before_sm[i];
-    const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
     auto slot = [&](int k) { return (int64_t)(before + (w.p.backward ? n - 1 - k : k)) * w.p.Hv + h; };
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (w.p.init) run = *reinterpret_cast<const float4*>(w.p.init + ((int64_t)seq * w.p.Hv + h) * (kD * kD) + e);
@@ -98,6 +93,51 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_con
                     run.w = fmaf(decay[k], run.w, own[k].w);
                 }
             }
+    }
+}
+
+__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_constant__ Walk w) {
+    const int h = blockIdx.x % w.p.Hv;
+    for (int seq = blockIdx.x / w.p.Hv; seq < w.p.n_seq; seq += kScanSeqs)
+        scan_sequence(w, seq, h, (blockIdx.y * kScanThreads + threadIdx.x) * 4);
+}
+
+// The parts of many sequences, written out (Walk's lists).  One CTA.
+constexpr int kListThreads = 1024;
+
+__global__ void __launch_bounds__(kListThreads)
+lin_parts_kernel(const __grid_constant__ Walk w, int32_t* part_seq, int32_t* inner, int32_t* seq_first) {
+    __shared__ int32_t sums[kListThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int32_t i = tid; i < w.n_parts; i += kListThreads) part_seq[i] = -1;
+    for (int32_t i = tid; i < w.n_inner; i += kListThreads) inner[i] = -1;
+    __syncthreads();
+    int32_t before = 0;                         // parts of the sequences in front of this block's
+    for (int32_t i0 = 0; i0 < w.p.n_seq; i0 += kListThreads) {
+        const int32_t i = i0 + tid;
+        const int32_t n = i < w.p.n_seq ? parts_of(w, w.p.cu[i], w.p.cu[i + 1]) : 0;
+        int32_t upto = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += x;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        int32_t all = 0;
+        for (int k = 0; k < kListThreads / 32; ++k) {
+            if (k < warp) upto += sums[k];
+            all += sums[k];
+        }
+        __syncthreads();
+        if (i < w.p.n_seq) {
+            const int32_t first = before + upto - n;
+            seq_first[i] = first;
+            if (i + 1 == w.p.n_seq) seq_first[i + 1] = first + n;
+            for (int32_t k = 0; k < n; ++k) part_seq[first + k] = i;
+            for (int32_t k = 0; k + 1 < n; ++k) inner[first - i + k] = first + k;
+        }
+        before += all;
     }
 }
 
@@ -149,7 +189,7 @@ lin_dg_kernel(const __grid_constant__ Walk w, const __grid_constant__ DgArgs a) 
     const int Hv = w.p.Hv;
     const int32_t index = blockIdx.x / Hv;
     const int h = blockIdx.x % Hv, tid = threadIdx.x;
-    const Part part = find_part(w, index);
+    const Part part = find_part(w, index, false);
     if (part.seq < 0 || part.t1 == part.t0) {
         if (a.part_sum && tid == 0) a.part_sum[(int64_t)index * Hv + h] = 0.0;
         return;
@@ -292,8 +332,9 @@ cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
         (kMode != kState && (!make_map(&mx, w.p.x, w.p.T, w.p.Hv) || !make_out_map(&mo, w.p))) ||
         (kMode == kExact && !make_map(&mu, w.p.u, w.p.T, w.p.Hv)))
         return cudaErrorInvalidValue;
-    const int64_t blocks = (int64_t)w.n_parts * (kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep);
+    const int64_t blocks = kMode == kState ? (int64_t)w.n_inner * w.p.Hv : (int64_t)w.n_parts * (w.p.Hv / w.p.out_rep);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (blocks == 0) return cudaSuccess;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(lin_walk_kernel<kMode>), Layout<kMode>::kAlloc, allowed[kMode]);
     if (e != cudaSuccess) return e;
     lin_walk_kernel<kMode><<<(unsigned)blocks, kThreads, Layout<kMode>::kAlloc, s>>>(mx, my, mz, mu, mo, w);
@@ -312,7 +353,8 @@ cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
 cudaError_t launch_joints(const Walk& w, cudaStream_t s) {
     cudaError_t e = launch_walk<kState>(w, s);
     if (e != cudaSuccess) return e;
-    lin_scan_kernel<<<dim3((unsigned)(w.p.n_seq * w.p.Hv), kD * kD / (kScanThreads * 4)), kScanThreads, 0, s>>>(w);
+    const int seqs = w.p.n_seq < kScanSeqs ? w.p.n_seq : kScanSeqs;
+    lin_scan_kernel<<<dim3((unsigned)(seqs * w.p.Hv), kD * kD / (kScanThreads * 4)), kScanThreads, 0, s>>>(w);
     return cudaGetLastError();
 }
 
@@ -324,26 +366,43 @@ cudaError_t pass_state(const float* from, float* to, int32_t n_seq, int32_t Hv, 
 }
 
 struct Joints {
-    int32_t part_len, n_parts, split;
-    size_t state_bytes, decay_bytes;
+    int32_t part_len, n_parts, n_inner, split;
+    size_t state_bytes, decay_bytes, list_bytes;
 };
 
 Joints plan_joints(int32_t n_seq, int64_t T, int32_t Hv, int32_t heads, int64_t most) {
     Joints j;
     j.part_len = choose_part_len(n_seq, T, heads, Hv / heads, most);
     j.n_parts = part_count(n_seq, T, j.part_len);
+    j.n_inner = (int32_t)(T / j.part_len);      // parts that are not the last of their sequence are whole
     j.split = T > j.part_len;
     if (!j.split) j.n_parts = n_seq;
     j.state_bytes = j.split ? up256((size_t)j.n_parts * Hv * kD * kD * 4) : 0;
     j.decay_bytes = j.split ? up256((size_t)j.n_parts * Hv * 4) : 0;
+    // (a CTA of the kernels finds its part among up to 32 sequences itself)
+    j.list_bytes = j.split && n_seq > 32 ? up256(((size_t)j.n_parts + j.n_inner + n_seq + 1) * 4) : 0;
     return j;
+}
+
+// fills in w's parts, writing the lists where there are any
+cudaError_t set_parts(Walk& w, const Joints& j, char* lists, cudaStream_t s) {
+    w.part_len = j.part_len; w.n_parts = j.n_parts; w.n_inner = j.n_inner; w.split = j.split;
+    if (j.list_bytes == 0) return cudaSuccess;
+    int32_t* part_seq = reinterpret_cast<int32_t*>(lists);
+    int32_t* inner = part_seq + j.n_parts;
+    int32_t* seq_first = inner + j.n_inner;
+    w.part_seq = part_seq;
+    w.inner = inner;
+    w.seq_first = seq_first;
+    lin_parts_kernel<<<1, kListThreads, 0, s>>>(w, part_seq, inner, seq_first);
+    return cudaGetLastError();
 }
 
 constexpr int64_t kAnyLength = (int64_t)1 << 30;
 
 struct BackwardPlan {
     Joints j;
-    size_t qdq, kdk, acc, fin, sums, fwd, bwd, decay_f, decay_b, bytes;
+    size_t qdq, kdk, acc, fin, sums, fwd, bwd, decay_f, decay_b, lists, bytes;
 };
 
 BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
@@ -361,6 +420,7 @@ BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
     b.bwd = take(b.j.state_bytes);
     b.decay_f = take(b.j.decay_bytes);
     b.decay_b = take(b.j.decay_bytes);
+    b.lists = take(b.j.list_bytes);
     b.bytes = off;
     return b;
 }
@@ -369,7 +429,7 @@ BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
 
 size_t linear_prefill_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hv) {
     const Joints j = plan_joints(n_seq, T, Hv, Hv, kAnyLength);
-    return kWsHeaderBytes + j.state_bytes + j.decay_bytes;
+    return kWsHeaderBytes + j.state_bytes + j.decay_bytes + j.list_bytes;
 }
 
 cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
@@ -379,7 +439,6 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
     if (a.T == 0) return pass_state(a.initial_state, a.final_state, a.n_seq, a.Hv, s);
     const Joints j = plan_joints(a.n_seq, a.T, a.Hv, a.Hv, kAnyLength);
     Walk w{};
-    w.part_len = j.part_len; w.n_parts = j.n_parts; w.split = j.split;
     w.joint = reinterpret_cast<float*>(ws + kWsHeaderBytes);
     w.joint_decay = reinterpret_cast<float*>(ws + kWsHeaderBytes + j.state_bytes);
     w.err = reinterpret_cast<uint32_t*>(ws + kWsErrorWordOffset);
@@ -390,6 +449,8 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
     p.g = a.g; p.ldg = a.ldg; p.cu = a.cu_seqlens; p.n_seq = a.n_seq; p.T = a.T; p.Hv = a.Hv; p.scale = a.scale;
     p.init = a.initial_state; p.fin = a.final_state;
     p.out = a.o; p.out_bf16 = a.o_bf16;
+    e = set_parts(w, j, ws + kWsHeaderBytes + j.state_bytes + j.decay_bytes, s);
+    if (e != cudaSuccess) return e;
     if (j.split && (e = launch_joints(w, s)) != cudaSuccess) return e;
     return launch_walk<kOut>(w, s);
 }
@@ -411,10 +472,10 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     const int rep = a.Hv / a.Hqk;
     const LinOperand q{a.q, a.ldq, rep}, k{a.k, a.ldk, rep}, v{a.v, a.ldv, 1}, d_o{a.d_o, (int64_t)a.Hv * kD, 1};
     Walk base{};
-    base.part_len = b.j.part_len; base.n_parts = b.j.n_parts; base.split = b.j.split;
     base.err = reinterpret_cast<uint32_t*>(ws + kWsErrorWordOffset);
     base.p.g = a.g; base.p.ldg = a.ldg; base.p.cu = a.cu_seqlens; base.p.n_seq = a.n_seq; base.p.T = a.T;
     base.p.Hv = a.Hv; base.p.scale = a.scale; base.p.out_bf16 = a.grad_bf16;
+    if ((e = set_parts(base, b.j, ws + b.lists, s)) != cudaSuccess) return e;
     Walk fwd = base, bwd = base;
     fwd.joint = floats(b.fwd); fwd.joint_decay = floats(b.decay_f);
     bwd.joint = floats(b.bwd); bwd.joint_decay = floats(b.decay_b);

@@ -82,51 +82,73 @@ struct Walk {
     int32_t joint_t;                // joint holds the transposed state
     float* joint_decay;             // [n_parts, Hv]
     uint32_t* err;
+    // with many sequences, their parts written out beforehand (else NULL): the sequence of each part (-1: no such
+    // part), the parts that are not their sequence's last, each sequence's first part
+    const int32_t* part_seq;        // [n_parts]
+    const int32_t* inner;           // [n_inner]
+    const int32_t* seq_first;       // [n_seq + 1]
+    int32_t n_inner;                // upper bound of the number of parts that are not the last
 };
 
 struct Part {
     int64_t t0, t1;                 // its tokens
     int32_t seq;                    // -1: there is no such part
+    int32_t slot;                   // its number among all parts
     int32_t first, last;            // first and last of its sequence, in the pass's direction
     int32_t alone;                  // its sequence has one part
 };
 
-// The index-th part: sequence i has max(1, ceil(len / part_len)) parts.  One warp.
-GDN_DEVICE Part find_part(const Walk& w, int32_t index) {
+// parts of a sequence: one at least
+GDN_DEVICE int32_t parts_of(const Walk& w, int32_t a, int32_t b) {
+    return b > a ? (int32_t)(((uint32_t)(b - a) + (uint32_t)w.part_len - 1u) / (uint32_t)w.part_len) : 1;
+}
+
+// The index-th part, or the index-th of those that are not the last of their sequence in the pass's direction.  One
+// warp; without the written-out lists at most 32 sequences.
+GDN_DEVICE Part find_part(const Walk& w, int32_t index, bool inner) {
     const int lane = threadIdx.x & 31;
-    Part r{0, 0, -1, 0, 0, 0};
-    const uint32_t len = (uint32_t)w.part_len;
-    int32_t before = 0;
-    for (int32_t i0 = 0; i0 < w.p.n_seq; i0 += 32) {
-        const int32_t i = i0 + lane;
-        int32_t a = 0, b = 0, n = 0;
-        if (i < w.p.n_seq) {
-            a = w.p.cu ? w.p.cu[i] : 0;
-            b = w.p.cu ? w.p.cu[i + 1] : (int32_t)w.p.T;
-            n = b > a ? (int32_t)(((uint32_t)(b - a) + len - 1u) / len) : 1;
+    Part r{0, 0, -1, index, 0, 0, 0};
+    const int skip = w.p.backward ? 1 : 0;      // backward in time a sequence's last part is its first one
+    int32_t k = 0, n = 1, a = 0, b = 0;
+    if (!w.split) {
+        if (index >= w.p.n_seq || inner) return r;
+        r.seq = index;
+    } else if (w.part_seq) {
+        if (inner) {
+            r.slot = index < w.n_inner ? w.inner[index] : -1;
+            if (r.slot < 0) return r;
+            r.slot += skip;
         }
-        int32_t upto = n;
+        r.seq = w.part_seq[r.slot];
+        if (r.seq < 0) return r;
+        const int32_t first = w.seq_first[r.seq];
+        k = r.slot - first;
+        n = w.seq_first[r.seq + 1] - first;
+    } else {
+        int32_t mine = 0;
+        if (lane < w.p.n_seq) mine = parts_of(w, w.p.cu ? w.p.cu[lane] : 0, w.p.cu ? w.p.cu[lane + 1] : (int32_t)w.p.T);
+        int32_t upto = mine;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const int32_t x = __shfl_up_sync(0xffffffffu, upto, m);
             if (lane >= m) upto += x;
         }
-        const int32_t k = index - before - (upto - n);                   // the part's number in this lane's sequence
-        const unsigned found = __ballot_sync(0xffffffffu, k >= 0 && k < n);
-        if (found) {
-            const int src = __ffs(found) - 1;
-            const int32_t s0 = __shfl_sync(0xffffffffu, a, src), s1 = __shfl_sync(0xffffffffu, b, src);
-            const int32_t kk = __shfl_sync(0xffffffffu, k, src), nn = __shfl_sync(0xffffffffu, n, src);
-            r.t0 = s0 + (int64_t)kk * len;
-            r.t1 = r.t0 + len < s1 ? r.t0 + len : s1;
-            r.seq = i0 + src;
-            r.first = w.p.backward ? kk == nn - 1 : kk == 0;
-            r.last = w.p.backward ? kk == 0 : kk == nn - 1;
-            r.alone = nn == 1;
-            return r;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        // the number in this lane's sequence (each of the sequences up to it has one part that is not inner)
+        const int32_t kk = inner ? index - (upto - mine - min(lane, w.p.n_seq)) : index - (upto - mine);
+        const unsigned found = __ballot_sync(0xffffffffu, kk >= 0 && kk < (inner ? mine - 1 : mine));
+        if (!found) return r;
+        r.seq = __ffs(found) - 1;
+        k = __shfl_sync(0xffffffffu, kk, r.seq) + (inner ? skip : 0);
+        n = __shfl_sync(0xffffffffu, mine, r.seq);
+        r.slot = __shfl_sync(0xffffffffu, upto, r.seq) - n + k;
     }
+    a = w.p.cu ? w.p.cu[r.seq] : 0;
+    b = w.p.cu ? w.p.cu[r.seq + 1] : (int32_t)w.p.T;
+    r.t0 = a + (int64_t)k * w.part_len;
+    r.t1 = r.t0 + w.part_len < b ? r.t0 + w.part_len : b;
+    r.first = w.p.backward ? k == n - 1 : k == 0;
+    r.last = w.p.backward ? k == 0 : k == n - 1;
+    r.alone = n == 1;
     return r;
 }
 
@@ -245,8 +267,7 @@ struct Ctx {
     volatile int* abort;
     uint32_t abort_at;              // its shared-space address
     Part part;
-    int32_t index;                  // of the part
-    int32_t chunks;                 // of it
+    int32_t chunks;                 // of the part
     int32_t head;                   // output head (kState: value head)
     int32_t reps;                   // value heads to take in turn
     int32_t head0;                  // the first of them
@@ -805,7 +826,7 @@ GDN_DEVICE void state_role(const Ctx& c) {
     for (int r = 0; r < c.reps; ++r) {
         const int h = c.head0 + r;
         const int64_t own = ((int64_t)c.part.seq * p.Hv + h) * (kD * kD);
-        const int64_t joint = ((int64_t)c.index * p.Hv + h) * (kD * kD);
+        const int64_t joint = ((int64_t)c.part.slot * p.Hv + h) * (kD * kD);
         // kOut: the last stage, which the loads leave alone until then
         uint8_t* room = kMode == kOut && r == 0 ? c.sm + (L::kStages - 1) * L::kStage + warp * 8192 : nullptr;
         if (kMode == kState) load_state(S, nullptr, false, z, half, nullptr);
@@ -1037,9 +1058,8 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     const int warp = threadIdx.x >> 5;
     const int heads = kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep;
     const int32_t index = (int32_t)(blockIdx.x / heads);
-    const Part part = find_part(w, index);
-    // kState: the last part's own sum is not needed
-    if (part.seq < 0 || (kMode == kState && part.last)) return;
+    const Part part = find_part(w, index, kMode == kState);       // (the last part's own sum is not needed)
+    if (part.seq < 0) return;
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 8);
     if (threadIdx.x == 0) {
         auto init = [&](int i, uint32_t n) { mbar_init(base + L::kBars + i * 8, n); };
@@ -1077,7 +1097,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kMisc);
     const int head = (int)(blockIdx.x - (unsigned)index * heads);
     const int reps = kMode == kState ? 1 : w.p.out_rep;
-    const Ctx c{w, sm, base, tmem, abort, base + L::kMisc + 8, part, index, (int32_t)((part.t1 - part.t0 + kC - 1) / kC), head, reps, head * reps};
+    const Ctx c{w, sm, base, tmem, abort, base + L::kMisc + 8, part, (int32_t)((part.t1 - part.t0 + kC - 1) / kC), head, reps, head * reps};
     if (warp < 8) {
         regs_inc<kRegsState>();
         state_role<kMode>(c);
@@ -1115,7 +1135,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         // the part's whole decay
         const long long* sum = reinterpret_cast<const long long*>(sm + L::kMisc + 16);
         const float* bad = reinterpret_cast<const float*>(sm + L::kMisc + 32);
-        w.joint_decay[(int64_t)index * w.p.Hv + head] =
+        w.joint_decay[(int64_t)part.slot * w.p.Hv + head] =
             exp2f((float)((double)(sum[0] + sum[1]) * (1.0 / 4294967296.0))) + bad[0] + bad[1];
     }
     if (warp == 25) tmem_dealloc(tmem, 512);

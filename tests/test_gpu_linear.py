@@ -271,6 +271,54 @@ def test_backward_of_no_tokens():
     assert torch.equal(r["d_initial_state"], dfin) and not r["dg"].any()
 
 
+def test_many_sequences():
+    """More sequences than a warp finds its part among, long, short and empty ones: some in several parts."""
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    lengths = [(37 * i) % 11 for i in range(70)] + [1400] + [(13 * i) % 7 for i in range(40)] + [700, 0]
+    c = Case(16, lengths, 1, 2)
+    q, k, v, g = c.dev()
+    cu, s0, dfin = dev_i32(c.cu), dev_f32(c.s0), dev_f32(c.dfin)
+    o, fin = gdn.linear_prefill(q, k, v, g, cu_seqlens=cu, scale=c.scale, initial_state=s0)
+    check_prefill(c, o, fin, True)
+    r = gdn.linear_prefill_backward(q, k, v, g, dev_bf16(c.dob), d_final_state=dfin, cu_seqlens=cu, scale=c.scale,
+                                    initial_state=s0)
+    check_backward(c, r, True)
+
+
+def test_rows_past_32_bits():
+    """A sequence whose rows start past 2^32 bytes gives what it gives alone ."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    Hv, n = 16, 1100
+    T = (1 << 32) // (Hv * D * 2) + n
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.zeros(T, Hv, D, dtype=torch.bfloat16, device="cuda")
+    q, k = (torch.zeros(T, 2, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.full((T, Hv), -0.05, device="cuda")
+    for x in (q, k, v):
+        x[-n:] = torch.randn(n, *x.shape[1:], generator=gen, device="cuda").bfloat16()
+    g[-n:] = -torch.rand(n, Hv, generator=gen, device="cuda")
+    cu = dev_i32([0, T - n, T])
+    o, fin = gdn.linear_prefill(q, k, v, g, cu_seqlens=cu)
+    assert not o[:T - n].any() and not fin[0].any()
+    small = [x[-n:].clone() for x in (q, k, v, g)]
+    o1, fin1 = gdn.linear_prefill(*small)
+    want, wfin, _ = ref.prefill(host(small[0]), host(small[1]), host(small[2]), host(small[3]), [0, n], D ** -0.5)
+    m, size = ref.sizes(host(small[0]), host(small[1]), host(small[2]), host(small[3]), [0, n], D ** -0.5)
+    for oo, ff in ((o[-n:], fin[1:]), (o1, fin1)):
+        close(oo, want, (B16 + f32_tol(n)) * m + B16 * np.abs(want) + 1e-30, "o")
+        close(ff, wfin, f32_tol(n) * size + 1e-30, "final_state")
+    d_o = torch.zeros_like(v)
+    d_o[-n:] = torch.randn(n, Hv, D, generator=gen, device="cuda").bfloat16()
+    r = gdn.linear_prefill_backward(q, k, v, g, d_o, cu_seqlens=cu)
+    r1 = gdn.linear_prefill_backward(*small, d_o[-n:].clone())
+    for name in ("dq", "dk", "dv", "dg"):
+        a, b = r[name][-n:].float(), r1[name].float()
+        # the cuts may differ: the same to the rounding of the result and of what enters it
+        assert (a - b).norm() <= 4 * B16 * b.norm(), name
+        assert not r[name][:T - n].any(), name
+
+
 # ---- one token ----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("n_seq,layers,Hqk,Hv", [(1, 1, 1, 1), (1, 3, 2, 6), (5, 2, 2, 4), (40, 2, 4, 12), (9, 7, 16, 48)])
@@ -407,6 +455,42 @@ def test_same_result_every_time_on_another_stream_and_replayed():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first, held))
+
+
+def test_two_calls_at_once():
+    """Two streams at a time, each with its own workspace."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    cases = [Case(41, [900, 33], 2, 4), Case(42, [64, 1200], 2, 4)]
+    dev = [(c.dev(), dev_i32(c.cu), dev_f32(c.s0)) for c in cases]
+    run = lambda d, s: gdn.linear_prefill(*d[0], cu_seqlens=d[1], initial_state=d[2], stream=s)  # noqa: E731
+    alone = [run(d, None) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    for _ in range(20):
+        both = [run(d, s) for d, s in zip(dev, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_decode_captured_and_replayed():
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v, g, S = r(6, 2, D).bfloat16(), r(6, 2, D).bfloat16(), r(6, 4, D).bfloat16(), -r(6, 4).abs(), r(8, 4, D, D)
+    slot, start = dev_i32([3, -1, 0]), S.clone()
+    o = gdn.linear_decode_step(q, k, v, g, S, 3, 2, slot=slot)
+    want = S.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = gdn.linear_decode_step(q, k, v, g, S, 3, 2, slot=slot)
+    S.copy_(start)
+    held.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(S, want) and torch.equal(held, o) and not o[2:4].any()
 
 
 def test_workspace_reports_no_timeout():

@@ -141,6 +141,9 @@ def test_state_pool_refuses(L):
     assert L.gdn_state_copy(ok, 1, 4, None, p(), 1, None) == 1
     assert L.gdn_state_copy(ok, 1, 4, p(FAKE + 2), p(), 1, None) == 3
     assert L.gdn_state_copy(ok, 1, 4, p(), p(), 0, None) == 0
+    twice = (StateBuffer * 2)(StateBuffer(0x10000, 64), StateBuffer(0x10080, 64))
+    assert L.gdn_state_copy(twice, 2, 4, p(), p(), 1, None) == 1                             # they overlap
+    assert L.gdn_state_copy(twice, 2, 2, p(), p(), 0, None) == 0
     ws = L.gdn_state_workspace_size(4)
     assert ws > 0
     assert L.gdn_state_fork(ok, 1, 4, p(), p(), p(), 2, p(0x20000), ws, None) == 1          # src is dst
