@@ -915,6 +915,9 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
             // lane / 4 (+ 8)
             const int tq = 2 * (lane & 3);
             const uint32_t stage = c.base + st * L::kStage;
+            uint32_t at32[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) at32[e] = sw128_off(tq + e, lane >> 4) + ((lane >> 2) & 3) * 4;
             // matrix m of 16 tokens and 16 z indices: tokens 8 (m >> 1), z indices 8 (m & 1)
             const int mt = ((lane >> 4) << 3) + (lane & 7), mz = quad * 32 + ((lane >> 3) & 1) * 8;
 #pragma unroll 1
@@ -927,6 +930,11 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                     float inter[8], out[8];
                     const uint32_t src = c.tmem + lanes + ((uint32_t)hz << 16) + half * 32 + tb;
                     tmem_ld_frag16x2w(src + L::tInter, src + L::tP + set * 64, inter, out);
+                    if (tb + hz == 32) {        // the last of this warp's: the products may go on
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bOFree));
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
                         const float2 x = fma2(e < 4 ? a0 : a1, make_float2(inter[e], inter[e + 1]),
@@ -947,13 +955,12 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                         }
                     }
                     if (f32) {
-                        // (conflict-free: a warp's rows put their 16-byte pieces in different places)
-                        uint8_t* to = c.sm + st * L::kStage + rows + quad * L::kRows;
-                        const int piece = (hz + (lane >> 2)) >> 2;
+                        // row tb + tq + 8 (e / 4) + e % 2, element hz + 8 (e / 2 % 2) + lane / 4 of the quadrant's 32: its
+                        // 16-byte piece is swizzled by the row, so a warp's rows put theirs in different places
+                        uint8_t* to = c.sm + st * L::kStage + rows + quad * L::kRows + tb * 128;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float*>(to + sw128_off(tb + tq + (e >> 2) * 8 + (e & 1), piece + ((e >> 1) & 1) * 2) +
-                                                      ((lane >> 2) & 3) * 4) = out[e];
+                            *reinterpret_cast<float*>(to + (e >> 2) * 1024 + (at32[e & 1] ^ (((e >> 1) & 1) << 5) ^ (hz << 2))) = out[e];
                     } else {
                         uint32_t v[4];
 #pragma unroll
@@ -977,12 +984,10 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                                                                   2 * (lane & 3) + (lane >> 3)] = k2;
                 }
             }
-            tc_fence_before();
             fence_async_smem();
             const bool whole = half * 32 + 32 <= valid;         // every row of this half is this part's
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(c.bar(L::kBars, L::bOFree));
                 mbar_arrive(c.bar(L::kBars, L::bRows + half));
                 if (whole && quad != 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
             }
