@@ -996,6 +996,13 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
             if (whole && quad != 0) continue;
             // the four warps of this half have their z indices in place
             if (!c.wait(L::kBars, L::bRows + half, now)) return;
+            if (kMode == kExact && quad == 0 && half * 32 + lane < valid) {
+                // (two buffers: the chunk after the next needs this stage, which this warp has not yet released)
+                static_assert(kMode != kExact || L::kStages == 2, "the buffers of the dot products");
+                const float* d = reinterpret_cast<const float*>(c.sm + L::kDots) + (now & 1u) * 256 + half * 128 + lane;
+                p.dots[(int64_t)(c.head0 + r) * p.T + t0 + half * 32 + lane] = (d[0] + d[32]) + (d[64] + d[96]);
+            }
+            __syncwarp();
             if (whole) {
                 if (lane == 0) {
                     const int32_t x = c.head * kD, y = (int32_t)t0 + half * 32;
@@ -1011,8 +1018,14 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                         }
                     }
                     bulk_commit();
+                    if (kMode == kExact) {
+                        // With two stages the next but one chunk's loads wait for these rows to leave: at once, not
+                        // at the next turn (7,100 cycles a chunk).
+                        bulk_wait_read();
+                        mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
+                    }
                 }
-                held = st;
+                if (kMode != kExact) held = st;
             } else {
                 // the part's last rows: those behind them are not this part's, so plain stores, 8 rows a warp
                 const int pieces = f32 ? 32 : 16;
@@ -1036,12 +1049,6 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                         *to = x;
                     }
                 }
-            }
-            if (kMode == kExact && quad == 0 && half * 32 + lane < valid) {
-                // (two buffers: the chunk after the next needs this stage, which this warp has not yet released)
-                static_assert(kMode != kExact || L::kStages == 2, "the buffers of the dot products");
-                const float* d = reinterpret_cast<const float*>(c.sm + L::kDots) + (now & 1u) * 256 + half * 128 + lane;
-                p.dots[(int64_t)(c.head0 + r) * p.T + t0 + half * 32 + lane] = (d[0] + d[32]) + (d[64] + d[96]);
             }
             __syncwarp();
             if (!whole && lane == 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
