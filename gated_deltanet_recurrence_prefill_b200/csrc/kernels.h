@@ -227,6 +227,7 @@ cudaError_t launch_linear_decode(const LinearDecodeArgs& a, cudaStream_t stream)
 
 // pages of a state cache (state_pool.cu)
 constexpr int kMaxStateBuffers = 8;
+constexpr int kMaxStateCopies = 1024;
 struct StateBuffers {
     uint8_t* data[kMaxStateBuffers];
     int64_t bytes[kMaxStateBuffers];       // of a slot

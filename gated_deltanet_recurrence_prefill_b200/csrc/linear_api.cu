@@ -45,7 +45,8 @@ gdn_status check_workspace(const void* workspace, size_t bytes, size_t need, uin
 }
 
 gdn_status check_buffers(const gdn_state_buffer* buffers, int32_t n_buffers, int32_t n_slots, gdn::StateBuffers& b) {
-    static_assert(GDN_MAX_STATE_BUFFERS == gdn::kMaxStateBuffers, "the header's limit");
+    static_assert(GDN_MAX_STATE_BUFFERS == gdn::kMaxStateBuffers && GDN_MAX_STATE_COPIES == gdn::kMaxStateCopies,
+                  "the header's limits");
     if (n_buffers < 0 || n_slots <= 0 || (n_buffers > 0 && !buffers)) return GDN_ERR_INVALID_ARG;
     if (n_buffers > GDN_MAX_STATE_BUFFERS || n_slots > (1 << 24)) return GDN_ERR_UNSUPPORTED;
     for (int i = 0; i < n_buffers; ++i) {

@@ -31,6 +31,8 @@ constexpr int kCopyThreads = 512;
 constexpr int kCopyStage = 48 * 1024;          // bytes of an item; a CTA has room for two, an SM for two CTAs
 constexpr int kCopyCtas = 2;
 constexpr int kCopyMinRange = 64;              // least bytes of a page in an item (1,024 entries: 128 KB of room)
+constexpr int kCopyMostSmem = kMaxStateCopies * (2 * kCopyMinRange + 8);
+static_assert(kCopyMostSmem >= 2 * kCopyStage + 8 * (kCopyStage / kCopyMinRange), "the most that any number of entries takes");
 
 __global__ void __launch_bounds__(kCopyThreads, kCopyCtas)
 state_copy_kernel(StateBuffers b, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int32_t n,
@@ -301,7 +303,8 @@ cudaError_t launch_state_copy(const StateBuffers& b, const int32_t* src, const i
     for (int k = 0; k < b.n; ++k) items += (b.bytes[k] + range - 1) / range;
     if (items == 0) return cudaSuccess;
     const size_t smem = 2 * (size_t)n * range + (size_t)n * 8;
-    cudaError_t e = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (one limit for every call: two at once must not lower it for each other)
+    cudaError_t e = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopyMostSmem);
     if (e != cudaSuccess) return e;
     const int64_t grid = items < 148 * kCopyCtas ? items : 148 * kCopyCtas;
     state_copy_kernel<<<(unsigned)grid, kCopyThreads, smem, s>>>(b, src, dst, n, range);

@@ -191,3 +191,38 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(b, want))
         assert all(torch.equal(x, y) for x, y in zip(first, held))
+
+
+def test_copies_of_few_and_many_pages_at_once():
+    """Calls from several threads, whose kernels need different amounts of shared memory."""
+    import threading
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    rng = np.random.default_rng(3)
+    sizes = (4, 700, 1024, 300)
+    lists = [[rng.permutation(n) for _ in range(60)] for n in sizes]
+    caches = [[torch.arange(n * 48, device="cuda", dtype=torch.int32).view(n, 48)] for n in sizes]
+    want = [c[0].cpu().numpy() for c in caches]
+    device = [[dev_i32(p) for p in l] for l in lists]
+    places = [dev_i32(np.arange(n)) for n in sizes]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(k):
+        try:
+            for p in device[k]:
+                gdn.state_copy(caches[k], p, places[k], stream=streams[k])
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for k in range(len(sizes)):
+        for p in lists[k]:
+            want[k] = want[k][p]
+        assert np.array_equal(caches[k][0].cpu().numpy(), want[k])
