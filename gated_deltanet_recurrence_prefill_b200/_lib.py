@@ -89,8 +89,6 @@ class StateBuffer(C.Structure):
     _fields_ = [("data", C.c_void_p), ("slot_bytes", C.c_int64)]
 
 
-
-
 class GdnError(RuntimeError):
     def __init__(self, fn: str, status: int):
         msg = f"{fn} failed: {STATUS.get(status, status)}"

@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int32_t kD = 128;
+constexpr int32_t kMostSlots = 1 << 24;           // of a cache, and entries of a list
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -48,7 +49,7 @@ gdn_status check_buffers(const gdn_state_buffer* buffers, int32_t n_buffers, int
     static_assert(GDN_MAX_STATE_BUFFERS == gdn::kMaxStateBuffers && GDN_MAX_STATE_COPIES == gdn::kMaxStateCopies,
                   "the header's limits");
     if (n_buffers < 0 || n_slots <= 0 || (n_buffers > 0 && !buffers)) return GDN_ERR_INVALID_ARG;
-    if (n_buffers > GDN_MAX_STATE_BUFFERS || n_slots > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    if (n_buffers > GDN_MAX_STATE_BUFFERS || n_slots > kMostSlots) return GDN_ERR_UNSUPPORTED;
     for (int i = 0; i < n_buffers; ++i) {
         if (!buffers[i].data || buffers[i].slot_bytes <= 0) return GDN_ERR_INVALID_ARG;
         if (!aligned(buffers[i].data, 16) || buffers[i].slot_bytes % 16 != 0) return GDN_ERR_MISALIGNED;
@@ -114,7 +115,8 @@ gdn_status gdn_linear_prefill_backward(const uint16_t* q, const uint16_t* k, con
     if (!flag(g_per_token) || !flag(grad_bf16)) return GDN_ERR_INVALID_ARG;
     if (!g_per_token && !dg) return GDN_ERR_INVALID_ARG;
     if (T > 0 && (!q || !k || !v || !g || !d_o || !dq || !dk || !dv || !dg)) return GDN_ERR_INVALID_ARG;
-    if (d_initial_state && d_initial_state == d_final_state) return GDN_ERR_INVALID_ARG;
+    if (d_initial_state && (d_initial_state == d_final_state || d_initial_state == initial_state))
+        return GDN_ERR_INVALID_ARG;
     if ((st = check_ld(ldq, Hqk)) != GDN_OK || (st = check_ld(ldk, Hqk)) != GDN_OK || (st = check_ld(ldv, Hv)) != GDN_OK)
         return st;
     const void* ptrs[] = {q, k, v, g, cu_seqlens, initial_state, d_o, d_final_state, dq, dk, dv, dg, d_initial_state};
@@ -170,8 +172,9 @@ gdn_status gdn_state_fork(const gdn_state_buffer* buffers, int32_t n_buffers, in
     gdn_status st = check_buffers(buffers, n_buffers, n_slots, b);
     if (st != GDN_OK) return st;
     if (n < 0 || !live) return GDN_ERR_INVALID_ARG;
+    if (n > kMostSlots) return GDN_ERR_UNSUPPORTED;
     if (n == 0) return GDN_OK;
-    if (!src || !dst || src == dst) return GDN_ERR_INVALID_ARG;
+    if (!src || !dst || src == dst || dst == live) return GDN_ERR_INVALID_ARG;
     if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(live, 4)) return GDN_ERR_MISALIGNED;
     if ((st = check_workspace(workspace, workspace_bytes, gdn::state_workspace_bytes(n_slots), 16)) != GDN_OK) return st;
     return done(gdn::launch_state_fork(b, live, src, dst, n, workspace, (cudaStream_t)stream));
@@ -182,7 +185,7 @@ gdn_status gdn_state_compact(const gdn_state_buffer* buffers, int32_t n_buffers,
     gdn::StateBuffers b;
     gdn_status st = check_buffers(buffers, n_buffers, n_slots, b);
     if (st != GDN_OK) return st;
-    if (!live || !moved) return GDN_ERR_INVALID_ARG;
+    if (!live || !moved || live == moved) return GDN_ERR_INVALID_ARG;
     if (!aligned(moved, 4) || !aligned(live, 4)) return GDN_ERR_MISALIGNED;
     if ((st = check_workspace(workspace, workspace_bytes, gdn::state_workspace_bytes(n_slots), 16)) != GDN_OK) return st;
     return done(gdn::launch_state_compact(b, live, moved, workspace, (cudaStream_t)stream));
@@ -190,6 +193,7 @@ gdn_status gdn_state_compact(const gdn_state_buffer* buffers, int32_t n_buffers,
 
 gdn_status gdn_state_free(int32_t* live, int32_t n_slots, const int32_t* slots, int32_t n, gdn_stream_t stream) {
     if (n_slots <= 0 || n < 0 || !live) return GDN_ERR_INVALID_ARG;
+    if (n_slots > kMostSlots || n > kMostSlots) return GDN_ERR_UNSUPPORTED;
     if (n == 0) return GDN_OK;
     if (!slots) return GDN_ERR_INVALID_ARG;
     if (!aligned(slots, 4) || !aligned(live, 4)) return GDN_ERR_MISALIGNED;

@@ -664,7 +664,7 @@ size_t gdn_linear_prefill_backward_workspace_size(int32_t n_seq, int64_t T, int3
  *                 head) and dv [T, Hv, d], all float32 (grad_bf16 = 0) or bf16 (1).
  *  dg             float32, shaped as g ([Hv]: summed over all tokens).
  *  d_initial_state [n_seq, Hv, d_v, d_k] float32 or NULL (not written); may not be
- *                 d_final_state.
+ *                 d_final_state or initial_state.
  * No atomics: the result is deterministic.  dg and d_initial_state are exact to
  * float32 rounding; dq, dk and dv as o in the prefill.  A log decay at or below
  * -104 has gradient 0.
@@ -709,7 +709,10 @@ typedef struct gdn_state_buffer {
     int64_t slot_bytes;    /* bytes of one slot, a positive multiple of 16 */
 } gdn_state_buffer;
 
-/* At most this many buffers per call (GDN_ERR_UNSUPPORTED above), and this many entries in a copy. */
+/*
+ * At most this many buffers per call, and this many entries in a copy; other lists and caches have at most 2^24 entries
+ * and slots (GDN_ERR_UNSUPPORTED above).  Buffers of one call must not overlap (GDN_ERR_INVALID_ARG).
+ */
 #define GDN_MAX_STATE_BUFFERS 8
 #define GDN_MAX_STATE_COPIES 1024
 
@@ -735,7 +738,8 @@ size_t gdn_state_workspace_size(int32_t n_slots);
  *  src   [n] int32: -1 or a live slot.  Any other entry takes none (dst[i] = -1).
  *  dst   [n] int32 output.  Free slots are given out in rising order, to the
  *        entries in order; where they run out, dst[i] = -1.
- *  workspace  gdn_state_workspace_size() bytes, 16-byte aligned.
+ *  workspace  gdn_state_workspace_size() bytes, 16-byte aligned; calls that share it must be ordered on one stream.
+ * live, src and dst are arrays of their own.
  */
 gdn_status gdn_state_fork(const gdn_state_buffer* buffers, int32_t n_buffers, int32_t n_slots, int32_t* live,
                           const int32_t* src, int32_t* dst, int32_t n, void* workspace, size_t workspace_bytes,

@@ -157,6 +157,22 @@ def test_state_pool_refuses(L):
     assert L.gdn_state_free(p(), 4, None, 0, None) == 0
 
 
+def test_refuses_long_lists_and_outputs_in_place_of_inputs(L):
+    from gated_deltanet_recurrence_prefill_b200._lib import StateBuffer
+    b = (StateBuffer * 1)(StateBuffer(0x10000, 64))
+    ws = L.gdn_state_workspace_size(4)
+    a1, a2, w, most = p(0x11000), p(0x12000), p(0x20000), 2 ** 31 - 1
+    assert L.gdn_state_fork(b, 1, 4, p(), a1, a2, most, w, ws, None) == 2
+    assert L.gdn_state_fork(b, 1, 4, p(), a1, p(), 2, w, ws, None) == 1                     # dst is live
+    assert L.gdn_state_compact(b, 1, 4, p(), p(), w, ws, None) == 1                         # moved is live
+    assert L.gdn_state_free(p(), 4, a1, most, None) == 2
+    assert L.gdn_state_free(p(), most, a1, 1, None) == 2
+    ws = L.gdn_linear_prefill_backward_workspace_size(1, 64, 16, 48, 128)
+    s0 = p(0x30000)
+    assert L.gdn_linear_prefill_backward(p(), p(), p(), 0, 0, 0, p(), 1, None, 1, 64, 16, 48, 128, 0.1, s0, p(), None,
+                                         p(), p(), p(), 1, p(), s0, w, ws, None) == 1       # d_initial is initial
+
+
 def test_binding_refuses_host_tensors_and_shapes():
     import torch
     import gated_deltanet_recurrence_prefill_b200 as gdn
