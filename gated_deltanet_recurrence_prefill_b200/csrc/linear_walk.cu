@@ -4,6 +4,7 @@
 
 #include <atomic>
 
+#include "launch_chain.h"
 #include "linear_walk.cuh"
 
 namespace gdn {
@@ -97,6 +98,8 @@ GDN_DEVICE void scan_sequence(const Walk& w, int seq, int h, int e) {
 }
 
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_constant__ Walk w) {
+    grid_wait();
+    grid_next();
     const int h = blockIdx.x % w.p.Hv;
     for (int seq = blockIdx.x / w.p.Hv; seq < w.p.n_seq; seq += kScanSeqs)
         scan_sequence(w, seq, h, (blockIdx.y * kScanThreads + threadIdx.x) * 4);
@@ -109,6 +112,9 @@ __global__ void __launch_bounds__(kListThreads)
 lin_parts_kernel(const __grid_constant__ Walk w, int32_t* part_seq, int32_t* inner, int32_t* seq_first) {
     __shared__ int32_t sums[kListThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_wait();
+    grid_next();
+    if (tid == 0) *w.err = 0u;
     for (int32_t i = tid; i < w.n_parts; i += kListThreads) part_seq[i] = -1;
     for (int32_t i = tid; i < w.n_inner; i += kListThreads) inner[i] = -1;
     __syncthreads();
@@ -161,15 +167,17 @@ GDN_DEVICE double block_sum(double x, double* sm) {
     return s;
 }
 
-// <a, b> of two states, 0 if one is NULL
+// <a, b> of two states, 0 if one is NULL: 16 products to a float32 sum, whose rounding is that of the states'
+// elements themselves, the sums' sum in 64 bits (all of it in 64 bits took the kernel 31 us at 8,192 tokens)
 GDN_DEVICE double state_product(const float* a, const float* b, double* sm) {
     if (!a || !b) return 0.0;
-    double s = 0.0;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int i = threadIdx.x * 4; i < kD * kD; i += kDgThreads * 4) {
         const float4 x = *reinterpret_cast<const float4*>(a + i), y = *reinterpret_cast<const float4*>(b + i);
-        s += ((double)x.x * y.x + (double)x.y * y.y) + ((double)x.z * y.z + (double)x.w * y.w);
+        s = make_float4(fmaf(x.x, y.x, s.x), fmaf(x.y, y.y, s.y), fmaf(x.z, y.z, s.z), fmaf(x.w, y.w, s.w));
     }
-    return block_sum(s, sm);
+    return block_sum(((double)s.x + s.y) + ((double)s.z + s.w), sm);
 }
 
 struct DgArgs {
@@ -186,6 +194,8 @@ struct DgArgs {
 __global__ void __launch_bounds__(kDgThreads)
 lin_dg_kernel(const __grid_constant__ Walk w, const __grid_constant__ DgArgs a) {
     __shared__ double sm[kDgThreads / 32];
+    grid_wait();
+    grid_next();
     const int Hv = w.p.Hv;
     const int32_t index = blockIdx.x / Hv;
     const int h = blockIdx.x % Hv, tid = threadIdx.x;
@@ -245,6 +255,7 @@ lin_dg_kernel(const __grid_constant__ Walk w, const __grid_constant__ DgArgs a) 
 // dg of decays that all tokens share: the parts' sums, one warp per head
 __global__ void lin_dg_sum_kernel(const double* part_sum, int32_t n_parts, int32_t Hv, float* dg) {
     const int h = blockIdx.x, lane = threadIdx.x;
+    grid_wait();
     double s = 0.0;
     for (int i = lane; i < n_parts; i += 32) s += part_sum[(int64_t)i * Hv + h];
 #pragma unroll
@@ -255,6 +266,8 @@ __global__ void lin_dg_sum_kernel(const double* part_sum, int32_t n_parts, int32
 // acc [tokens, width] in float32 -> out in bf16, for the tokens that sequences own; 8 elements a thread
 __global__ void __launch_bounds__(256) lin_round_kernel(const float* acc, uint16_t* out, const int32_t* cu, int32_t n_seq,
                                                         int64_t T, int32_t width) {
+    grid_wait();
+    grid_next();
     const int64_t n = (cu ? (int64_t)cu[n_seq] : T) * (width / 8);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const float4 a = reinterpret_cast<const float4*>(acc)[2 * i], b = reinterpret_cast<const float4*>(acc)[2 * i + 1];
@@ -326,7 +339,7 @@ cudaError_t allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>
 }
 
 template <int kMode>
-cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
+cudaError_t launch_walk(Walk w, Chain& chain) {
     CUtensorMap mx{}, my{}, mz{}, mu{}, mo{};
     if (!make_map(&my, w.p.y, w.p.T, w.p.Hv) || !make_map(&mz, w.p.z, w.p.T, w.p.Hv) ||
         (kMode != kState && (!make_map(&mx, w.p.x, w.p.T, w.p.Hv) || !make_out_map(&mo, w.p))) ||
@@ -337,25 +350,25 @@ cudaError_t launch_walk(const Walk& w, cudaStream_t s) {
     if (blocks == 0) return cudaSuccess;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(lin_walk_kernel<kMode>), Layout<kMode>::kAlloc, allowed[kMode]);
     if (e != cudaSuccess) return e;
-    lin_walk_kernel<kMode><<<(unsigned)blocks, kThreads, Layout<kMode>::kAlloc, s>>>(mx, my, mz, mu, mo, w);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    w.opens = !chain.begun;
+    e = chain.launch(true, lin_walk_kernel<kMode>, (unsigned)blocks, kThreads, Layout<kMode>::kAlloc, mx, my, mz, mu, mo, w);
+    if (e != cudaSuccess) return e;
     if (kMode != kState && w.p.out_rep > 1 && w.p.out_bf16) {
         const int32_t width = w.p.Hv / w.p.out_rep * kD;
         const int64_t n = (w.p.T * (width / 8) + 255) / 256;
-        lin_round_kernel<<<(unsigned)(n < kSms * 8 ? n : kSms * 8), 256, 0, s>>>(
-            w.p.acc, static_cast<uint16_t*>(w.p.out), w.p.cu, w.p.n_seq, w.p.T, width);
-        e = cudaGetLastError();
+        e = chain.launch(true, lin_round_kernel, (unsigned)(n < kSms * 8 ? n : kSms * 8), 256, 0, w.p.acc,
+                         static_cast<uint16_t*>(w.p.out), w.p.cu, w.p.n_seq, w.p.T, width);
     }
     return e;
 }
 
 // the starting states of all parts: each part's own sum, then the scan
-cudaError_t launch_joints(const Walk& w, cudaStream_t s) {
-    cudaError_t e = launch_walk<kState>(w, s);
+cudaError_t launch_joints(const Walk& w, Chain& chain) {
+    cudaError_t e = launch_walk<kState>(w, chain);
     if (e != cudaSuccess) return e;
     const int seqs = w.p.n_seq < kScanSeqs ? w.p.n_seq : kScanSeqs;
-    lin_scan_kernel<<<dim3((unsigned)(seqs * w.p.Hv), kD * kD / (kScanThreads * 4)), kScanThreads, 0, s>>>(w);
-    return cudaGetLastError();
+    return chain.launch(true, lin_scan_kernel, dim3((unsigned)(seqs * w.p.Hv), kD * kD / (kScanThreads * 4)),
+                        kScanThreads, 0, w);
 }
 
 // no tokens at all: the states pass through
@@ -385,7 +398,7 @@ Joints plan_joints(int32_t n_seq, int64_t T, int32_t Hv, int32_t heads, int64_t 
 }
 
 // fills in w's parts, writing the lists where there are any
-cudaError_t set_parts(Walk& w, const Joints& j, char* lists, cudaStream_t s) {
+cudaError_t set_parts(Walk& w, const Joints& j, char* lists, Chain& chain) {
     w.part_len = j.part_len; w.n_parts = j.n_parts; w.n_inner = j.n_inner; w.split = j.split;
     if (j.list_bytes == 0) return cudaSuccess;
     int32_t* part_seq = reinterpret_cast<int32_t*>(lists);
@@ -394,8 +407,7 @@ cudaError_t set_parts(Walk& w, const Joints& j, char* lists, cudaStream_t s) {
     w.part_seq = part_seq;
     w.inner = inner;
     w.seq_first = seq_first;
-    lin_parts_kernel<<<1, kListThreads, 0, s>>>(w, part_seq, inner, seq_first);
-    return cudaGetLastError();
+    return chain.launch(false, lin_parts_kernel, 1, kListThreads, 0, w, part_seq, inner, seq_first);
 }
 
 constexpr int64_t kAnyLength = (int64_t)1 << 30;
@@ -434,9 +446,10 @@ size_t linear_prefill_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hv) {
 
 cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
     char* ws = static_cast<char*>(a.workspace);
-    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
-    if (e != cudaSuccess) return e;
-    if (a.T == 0) return pass_state(a.initial_state, a.final_state, a.n_seq, a.Hv, s);
+    if (a.T == 0) {
+        const cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
+        return e == cudaSuccess ? pass_state(a.initial_state, a.final_state, a.n_seq, a.Hv, s) : e;
+    }
     const Joints j = plan_joints(a.n_seq, a.T, a.Hv, a.Hv, kAnyLength);
     Walk w{};
     w.joint = reinterpret_cast<float*>(ws + kWsHeaderBytes);
@@ -449,10 +462,11 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
     p.g = a.g; p.ldg = a.ldg; p.cu = a.cu_seqlens; p.n_seq = a.n_seq; p.T = a.T; p.Hv = a.Hv; p.scale = a.scale;
     p.init = a.initial_state; p.fin = a.final_state;
     p.out = a.o; p.out_bf16 = a.o_bf16;
-    e = set_parts(w, j, ws + kWsHeaderBytes + j.state_bytes + j.decay_bytes, s);
+    Chain chain{s};
+    cudaError_t e = set_parts(w, j, ws + kWsHeaderBytes + j.state_bytes + j.decay_bytes, chain);
     if (e != cudaSuccess) return e;
-    if (j.split && (e = launch_joints(w, s)) != cudaSuccess) return e;
-    return launch_walk<kOut>(w, s);
+    if (j.split && (e = launch_joints(w, chain)) != cudaSuccess) return e;
+    return launch_walk<kOut>(w, chain);
 }
 
 size_t linear_backward_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
@@ -463,9 +477,9 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     const BackwardPlan b = backward_plan(a.n_seq, a.T, a.Hqk, a.Hv);
     char* ws = static_cast<char*>(a.workspace);
     auto floats = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     if (a.T == 0) {
+        if ((e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s)) != cudaSuccess) return e;
         e = pass_state(a.d_final_state, a.d_initial_state, a.n_seq, a.Hv, s);
         return e == cudaSuccess && !a.ldg ? cudaMemsetAsync(a.dg, 0, (size_t)a.Hv * 4, s) : e;
     }
@@ -475,7 +489,8 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     base.err = reinterpret_cast<uint32_t*>(ws + kWsErrorWordOffset);
     base.p.g = a.g; base.p.ldg = a.ldg; base.p.cu = a.cu_seqlens; base.p.n_seq = a.n_seq; base.p.T = a.T;
     base.p.Hv = a.Hv; base.p.scale = a.scale; base.p.out_bf16 = a.grad_bf16;
-    if ((e = set_parts(base, b.j, ws + b.lists, s)) != cudaSuccess) return e;
+    Chain chain{s};
+    if ((e = set_parts(base, b.j, ws + b.lists, chain)) != cudaSuccess) return e;
     Walk fwd = base, bwd = base;
     fwd.joint = floats(b.fwd); fwd.joint_decay = floats(b.decay_f);
     bwd.joint = floats(b.bwd); bwd.joint_decay = floats(b.decay_b);
@@ -483,34 +498,35 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     if (b.j.split) {                            // S at the parts' starts, dS at their ends
         Walk w = fwd;
         w.p.y = k; w.p.z = v; w.p.init = a.initial_state;
-        if ((e = launch_joints(w, s)) != cudaSuccess) return e;
+        if ((e = launch_joints(w, chain)) != cudaSuccess) return e;
         w = bwd;
         w.p.y = q; w.p.z = d_o; w.p.init = a.d_final_state;
-        if ((e = launch_joints(w, s)) != cudaSuccess) return e;
+        if ((e = launch_joints(w, chain)) != cudaSuccess) return e;
     }
     float* fin = a.d_final_state ? floats(b.fin) : nullptr;
     Walk w = fwd;                               // dq: its state is S^T
     w.p.x = d_o; w.p.y = v; w.p.z = k; w.p.u = q; w.p.dots = floats(b.qdq);
     w.p.init = a.initial_state; w.p.fin = fin; w.p.state_t = 1; w.joint_t = 1;
     w.p.out = a.dq; w.p.out_rep = rep; w.p.acc = floats(b.acc);
-    if ((e = launch_walk<kExact>(w, s)) != cudaSuccess) return e;
+    if ((e = launch_walk<kExact>(w, chain)) != cudaSuccess) return e;
     w = bwd;                                    // dk: dS^T
     w.p.x = v; w.p.y = d_o; w.p.z = q; w.p.u = k; w.p.dots = floats(b.kdk);
     w.p.init = a.d_final_state; w.p.state_t = 1; w.joint_t = 1;
     w.p.out = a.dk; w.p.out_rep = rep; w.p.acc = floats(b.acc);
-    if ((e = launch_walk<kExact>(w, s)) != cudaSuccess) return e;
+    if ((e = launch_walk<kExact>(w, chain)) != cudaSuccess) return e;
     w = bwd;                                    // dv: dS
     w.p.x = k; w.p.y = q; w.p.z = d_o;
     w.p.init = a.d_final_state; w.p.fin = a.d_initial_state;
     w.p.out = a.dv;
-    if ((e = launch_walk<kOut>(w, s)) != cudaSuccess) return e;
+    if ((e = launch_walk<kOut>(w, chain)) != cudaSuccess) return e;
     double* sums = a.ldg ? nullptr : reinterpret_cast<double*>(ws + b.sums);
     fwd.p.init = a.initial_state;
     const DgArgs dg{floats(b.qdq), floats(b.kdk), bwd.joint, fin, a.d_final_state, a.d_initial_state, a.dg, sums};
-    lin_dg_kernel<<<(unsigned)(b.j.n_parts * a.Hv), kDgThreads, 0, s>>>(fwd, dg);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.ldg) return e;
-    lin_dg_sum_kernel<<<a.Hv, 32, 0, s>>>(sums, b.j.n_parts, a.Hv, a.dg);
-    return cudaGetLastError();
+    // (not ahead of time: its CTAs, eight to an SM, then crowd the SMs that fall free first, 670 us for 655 at 8,192
+    // tokens)
+    e = chain.launch(false, lin_dg_kernel, (unsigned)(b.j.n_parts * a.Hv), kDgThreads, 0, fwd, dg);
+    if (e != cudaSuccess || a.ldg) return e;
+    return chain.launch(false, lin_dg_sum_kernel, a.Hv, 32, 0, sums, b.j.n_parts, a.Hv, a.dg);
 }
 
 }  // namespace gdn

@@ -55,6 +55,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch_chain.h"
 #include "linear_attn.h"
 #include "tc_util.cuh"
 
@@ -82,6 +83,7 @@ struct Walk {
     int32_t joint_t;                // joint holds the transposed state
     float* joint_decay;             // [n_parts, Hv]
     uint32_t* err;
+    int32_t opens;                  // the first kernel of its call: clears the error word
     // with many sequences, their parts written out beforehand (else NULL): the sequence of each part (-1: no such
     // part), the parts that are not their sequence's last, each sequence's first part
     const int32_t* part_seq;        // [n_parts]
@@ -1070,8 +1072,14 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     const int warp = threadIdx.x >> 5;
     const int heads = kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep;
     const int32_t index = (int32_t)(blockIdx.x / heads);
+    // (well before any CTA can have waited long enough to raise it)
+    if (w.opens && blockIdx.x == 0 && threadIdx.x == 0) *w.err = 0u;
+    if (w.part_seq) grid_wait();                // the lists come from a kernel before
     const Part part = find_part(w, index, kMode == kState);       // (the last part's own sum is not needed)
-    if (part.seq < 0) return;
+    if (part.seq < 0) {
+        grid_wait();
+        return;
+    }
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::kMisc + 8);
     if (threadIdx.x == 0) {
         auto init = [&](int i, uint32_t n) { mbar_init(base + L::kBars + i * 8, n); };
@@ -1106,6 +1114,8 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();
+    grid_next();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kMisc);
     const int head = (int)(blockIdx.x - (unsigned)index * heads);
     const int reps = kMode == kState ? 1 : w.p.out_rep;

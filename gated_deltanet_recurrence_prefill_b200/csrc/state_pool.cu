@@ -7,6 +7,7 @@
 // kernels whose time does not show, and the moves run on every SM.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch_chain.h"
 
 namespace gdn {
 
@@ -170,6 +171,7 @@ GDN_DEVICE int block_rank(bool x, int* sums, int* total) {
 __global__ void __launch_bounds__(kPlanThreads)
 state_fork_plan_kernel(int32_t n_slots, int32_t* live, const int32_t* src, int32_t* dst, int32_t n, MoveList list) {
     __shared__ int sums[kPlanThreads / 32];
+    grid_next();
     const int tid = threadIdx.x;
     // entries: -1 (a page of zeros) or a live slot
     int wanted = 0;
@@ -208,6 +210,7 @@ state_fork_plan_kernel(int32_t n_slots, int32_t* live, const int32_t* src, int32
 __global__ void __launch_bounds__(kPlanThreads)
 state_compact_plan_kernel(int32_t n_slots, int32_t* live, int32_t* moved, MoveList list) {
     __shared__ int sums[kPlanThreads / 32];
+    grid_next();
     const int tid = threadIdx.x;
     int n_live = 0;
     for (int s0 = 0; s0 < n_slots; s0 += kPlanThreads) {
@@ -249,6 +252,7 @@ constexpr int kMoveBytes = kMoveThreads * kMoveLoads * 16;
 constexpr int kMoveCtas = 16;                  // per SM
 
 __global__ void __launch_bounds__(kMoveThreads) state_move_kernel(StateBuffers b, MoveList list) {
+    grid_wait();
     const int64_t moves = *list.count;
     int64_t item = blockIdx.x;
     for (int k = 0; k < b.n; ++k) {
@@ -281,13 +285,12 @@ __global__ void state_free_kernel(int32_t* live, int32_t n_slots, const int32_t*
     if (i < n && slots[i] >= 0 && slots[i] < n_slots) live[slots[i]] = 0;
 }
 
-cudaError_t launch_moves(const StateBuffers& b, const MoveList& list, int64_t most, cudaStream_t s) {
+cudaError_t launch_moves(const StateBuffers& b, const MoveList& list, int64_t most, Chain& chain) {
     int64_t items = 0;
     for (int k = 0; k < b.n; ++k) items += (b.bytes[k] + kMoveBytes - 1) / kMoveBytes * most;
     if (items == 0) return cudaSuccess;
     const int64_t grid = items < 148 * kMoveCtas ? items : 148 * kMoveCtas;
-    state_move_kernel<<<(unsigned)grid, kMoveThreads, 0, s>>>(b, list);
-    return cudaGetLastError();
+    return chain.launch(true, state_move_kernel, (unsigned)grid, kMoveThreads, 0, b, list);
 }
 
 }  // namespace
@@ -314,17 +317,17 @@ cudaError_t launch_state_copy(const StateBuffers& b, const int32_t* src, const i
 cudaError_t launch_state_fork(const StateBuffers& b, int32_t* live, const int32_t* src, int32_t* dst, int32_t n,
                               void* workspace, cudaStream_t s) {
     const MoveList list = move_list(workspace, b.n_slots);
-    state_fork_plan_kernel<<<1, kPlanThreads, 0, s>>>(b.n_slots, live, src, dst, n, list);
-    cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? launch_moves(b, list, n < b.n_slots ? n : b.n_slots, s) : e;
+    Chain chain{s};
+    const cudaError_t e = chain.launch(false, state_fork_plan_kernel, 1, kPlanThreads, 0, b.n_slots, live, src, dst, n, list);
+    return e == cudaSuccess ? launch_moves(b, list, n < b.n_slots ? n : b.n_slots, chain) : e;
 }
 
 cudaError_t launch_state_compact(const StateBuffers& b, int32_t* live, int32_t* moved, void* workspace,
                                  cudaStream_t s) {
     const MoveList list = move_list(workspace, b.n_slots);
-    state_compact_plan_kernel<<<1, kPlanThreads, 0, s>>>(b.n_slots, live, moved, list);
-    cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? launch_moves(b, list, b.n_slots / 2, s) : e;
+    Chain chain{s};
+    const cudaError_t e = chain.launch(false, state_compact_plan_kernel, 1, kPlanThreads, 0, b.n_slots, live, moved, list);
+    return e == cudaSuccess ? launch_moves(b, list, b.n_slots / 2, chain) : e;
 }
 
 cudaError_t launch_state_free(int32_t* live, int32_t n_slots, const int32_t* slots, int32_t n, cudaStream_t s) {
