@@ -97,7 +97,8 @@ GDN_DEVICE void scan_sequence(const Walk& w, int seq, int h, int e) {
     }
 }
 
-__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_constant__ Walk w) {
+__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(const __grid_constant__ WalkPair pair) {
+    const Walk& w = pair.w[blockIdx.z];
     grid_wait();
     grid_next();
     const int h = blockIdx.x % w.p.Hv;
@@ -263,11 +264,19 @@ __global__ void lin_dg_sum_kernel(const double* part_sum, int32_t n_parts, int32
     if (lane == 0) dg[h] = (float)s;
 }
 
-// acc [tokens, width] in float32 -> out in bf16, for the tokens that sequences own; 8 elements a thread
-__global__ void __launch_bounds__(256) lin_round_kernel(const float* acc, uint16_t* out, const int32_t* cu, int32_t n_seq,
-                                                        int64_t T, int32_t width) {
+// acc [tokens, width] in float32 -> out in bf16, for the tokens that sequences own; 8 elements a thread.  blockIdx.y:
+// which of two
+struct Rounds {
+    const float* acc[2];
+    uint16_t* out[2];
+};
+
+__global__ void __launch_bounds__(256)
+lin_round_kernel(const __grid_constant__ Rounds r, const int32_t* cu, int32_t n_seq, int64_t T, int32_t width) {
     grid_wait();
     grid_next();
+    const float* acc = r.acc[blockIdx.y];
+    uint16_t* out = r.out[blockIdx.y];
     const int64_t n = (cu ? (int64_t)cu[n_seq] : T) * (width / 8);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const float4 a = reinterpret_cast<const float4*>(acc)[2 * i], b = reinterpret_cast<const float4*>(acc)[2 * i + 1];
@@ -325,7 +334,7 @@ bool make_out_map(CUtensorMap* m, const LinPass& p) {
 }
 
 // raises a kernel's limit of dynamic shared memory, once per device (`done`: the devices where it has been)
-std::atomic<uint64_t> allowed[3];
+std::atomic<uint64_t> allowed[3][2];
 
 cudaError_t allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>& done) {
     int device = 0;
@@ -338,37 +347,52 @@ cudaError_t allow_smem(const void* kernel, uint32_t bytes, std::atomic<uint64_t>
     return e;
 }
 
-template <int kMode>
-cudaError_t launch_walk(Walk w, Chain& chain) {
-    CUtensorMap mx{}, my{}, mz{}, mu{}, mo{};
-    if (!make_map(&my, w.p.y, w.p.T, w.p.Hv) || !make_map(&mz, w.p.z, w.p.T, w.p.Hv) ||
-        (kMode != kState && (!make_map(&mx, w.p.x, w.p.T, w.p.Hv) || !make_out_map(&mo, w.p))) ||
-        (kMode == kExact && !make_map(&mu, w.p.u, w.p.T, w.p.Hv)))
-        return cudaErrorInvalidValue;
-    const int64_t blocks = kMode == kState ? (int64_t)w.n_inner * w.p.Hv : (int64_t)w.n_parts * (w.p.Hv / w.p.out_rep);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+// kPasses passes that share their parts, heads and shape
+template <int kMode, int kPasses>
+cudaError_t launch_walk(const Walk* w, Chain& chain) {
+    Passes<kPasses> ps{};
+    for (int i = 0; i < kPasses; ++i) {
+        const LinPass& p = w[i].p;
+        if (!make_map(&ps.y[i], p.y, p.T, p.Hv) || !make_map(&ps.z[i], p.z, p.T, p.Hv) ||
+            (kMode != kState && (!make_map(&ps.x[i], p.x, p.T, p.Hv) || !make_out_map(&ps.out[i], p))) ||
+            (kMode == kExact && !make_map(&ps.u[i], p.u, p.T, p.Hv)))
+            return cudaErrorInvalidValue;
+        ps.w[i] = w[i];
+    }
+    ps.w[0].opens = !chain.begun;
+    const LinPass& p = w[0].p;
+    const int64_t blocks = kMode == kState ? (int64_t)w[0].n_inner * p.Hv : (int64_t)w[0].n_parts * (p.Hv / p.out_rep);
+    if (blocks * kPasses > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(lin_walk_kernel<kMode>), Layout<kMode>::kAlloc, allowed[kMode]);
+    ps.blocks = (int32_t)blocks;
+    const auto kernel = lin_walk_kernel<kMode, kPasses>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Layout<kMode>::kAlloc, allowed[kMode][kPasses - 1]);
     if (e != cudaSuccess) return e;
-    w.opens = !chain.begun;
-    e = chain.launch(true, lin_walk_kernel<kMode>, (unsigned)blocks, kThreads, Layout<kMode>::kAlloc, mx, my, mz, mu, mo, w);
+    e = chain.launch(true, kernel, (unsigned)(blocks * kPasses), kThreads, Layout<kMode>::kAlloc, ps);
     if (e != cudaSuccess) return e;
-    if (kMode != kState && w.p.out_rep > 1 && w.p.out_bf16) {
-        const int32_t width = w.p.Hv / w.p.out_rep * kD;
-        const int64_t n = (w.p.T * (width / 8) + 255) / 256;
-        e = chain.launch(true, lin_round_kernel, (unsigned)(n < kSms * 8 ? n : kSms * 8), 256, 0, w.p.acc,
-                         static_cast<uint16_t*>(w.p.out), w.p.cu, w.p.n_seq, w.p.T, width);
+    if (kMode != kState && p.out_rep > 1 && p.out_bf16) {
+        const int32_t width = p.Hv / p.out_rep * kD;
+        const int64_t rows = (p.T * (width / 8) + 255) / 256;
+        Rounds r{};
+        for (int i = 0; i < kPasses; ++i) {
+            r.acc[i] = w[i].p.acc;
+            r.out[i] = static_cast<uint16_t*>(w[i].p.out);
+        }
+        e = chain.launch(true, lin_round_kernel, dim3((unsigned)(rows < kSms * 8 ? rows : kSms * 8), kPasses), 256, 0,
+                         r, p.cu, p.n_seq, p.T, width);
     }
     return e;
 }
 
 // the starting states of all parts: each part's own sum, then the scan
-cudaError_t launch_joints(const Walk& w, Chain& chain) {
-    cudaError_t e = launch_walk<kState>(w, chain);
+template <int kPasses>
+cudaError_t launch_joints(const WalkPair& w, Chain& chain) {
+    cudaError_t e = launch_walk<kState, kPasses>(w.w, chain);
     if (e != cudaSuccess) return e;
-    const int seqs = w.p.n_seq < kScanSeqs ? w.p.n_seq : kScanSeqs;
-    return chain.launch(true, lin_scan_kernel, dim3((unsigned)(seqs * w.p.Hv), kD * kD / (kScanThreads * 4)),
-                        kScanThreads, 0, w);
+    const LinPass& p = w.w[0].p;
+    const int seqs = p.n_seq < kScanSeqs ? p.n_seq : kScanSeqs;
+    return chain.launch(true, lin_scan_kernel,
+                        dim3((unsigned)(seqs * p.Hv), kD * kD / (kScanThreads * 4), kPasses), kScanThreads, 0, w);
 }
 
 // no tokens at all: the states pass through
@@ -414,7 +438,8 @@ constexpr int64_t kAnyLength = (int64_t)1 << 30;
 
 struct BackwardPlan {
     Joints j;
-    size_t qdq, kdk, acc, fin, sums, fwd, bwd, decay_f, decay_b, lists, bytes;
+    int32_t pair;                   // dq and dk in one launch
+    size_t qdq, kdk, acc, acc2, fin, sums, fwd, bwd, decay_f, decay_b, lists, bytes;
 };
 
 BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
@@ -426,6 +451,11 @@ BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
     b.qdq = take((size_t)T * Hv * 4);
     b.kdk = take((size_t)T * Hv * 4);
     b.acc = take(Hv > Hqk ? (size_t)T * Hqk * kD * 4 : 0);
+    // Where both fill no more than one round of CTAs, they share it (572 ragged tokens, 24 CTAs each: 100 -> 81 us for
+    // the whole backward).  Beyond that they take turns, with one accumulator and the faster kernel for one pass
+    // (8,192 tokens, 144 CTAs each: 650 us, in one launch 735).
+    b.pair = 2 * (int64_t)b.j.n_parts * Hqk <= kSms;
+    b.acc2 = take(b.pair && Hv > Hqk ? (size_t)T * Hqk * kD * 4 : 0);
     b.fin = take((size_t)n_seq * Hv * kD * kD * 4);
     b.sums = take((size_t)b.j.n_parts * Hv * 8);
     b.fwd = take(b.j.state_bytes);
@@ -465,8 +495,8 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
     Chain chain{s};
     cudaError_t e = set_parts(w, j, ws + kWsHeaderBytes + j.state_bytes + j.decay_bytes, chain);
     if (e != cudaSuccess) return e;
-    if (j.split && (e = launch_joints(w, chain)) != cudaSuccess) return e;
-    return launch_walk<kOut>(w, chain);
+    if (j.split && (e = launch_joints<1>({{w}}, chain)) != cudaSuccess) return e;
+    return launch_walk<kOut, 1>(&w, chain);
 }
 
 size_t linear_backward_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
@@ -496,29 +526,32 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     bwd.joint = floats(b.bwd); bwd.joint_decay = floats(b.decay_b);
     bwd.p.backward = 1;
     if (b.j.split) {                            // S at the parts' starts, dS at their ends
-        Walk w = fwd;
-        w.p.y = k; w.p.z = v; w.p.init = a.initial_state;
-        if ((e = launch_joints(w, chain)) != cudaSuccess) return e;
-        w = bwd;
-        w.p.y = q; w.p.z = d_o; w.p.init = a.d_final_state;
-        if ((e = launch_joints(w, chain)) != cudaSuccess) return e;
+        WalkPair w{{fwd, bwd}};
+        w.w[0].p.y = k; w.w[0].p.z = v; w.w[0].p.init = a.initial_state;
+        w.w[1].p.y = q; w.w[1].p.z = d_o; w.w[1].p.init = a.d_final_state;
+        if ((e = launch_joints<2>(w, chain)) != cudaSuccess) return e;
     }
     float* fin = a.d_final_state ? floats(b.fin) : nullptr;
-    Walk w = fwd;                               // dq: its state is S^T
-    w.p.x = d_o; w.p.y = v; w.p.z = k; w.p.u = q; w.p.dots = floats(b.qdq);
-    w.p.init = a.initial_state; w.p.fin = fin; w.p.state_t = 1; w.joint_t = 1;
-    w.p.out = a.dq; w.p.out_rep = rep; w.p.acc = floats(b.acc);
-    if ((e = launch_walk<kExact>(w, chain)) != cudaSuccess) return e;
-    w = bwd;                                    // dk: dS^T
-    w.p.x = v; w.p.y = d_o; w.p.z = q; w.p.u = k; w.p.dots = floats(b.kdk);
-    w.p.init = a.d_final_state; w.p.state_t = 1; w.joint_t = 1;
-    w.p.out = a.dk; w.p.out_rep = rep; w.p.acc = floats(b.acc);
-    if ((e = launch_walk<kExact>(w, chain)) != cudaSuccess) return e;
-    w = bwd;                                    // dv: dS
+    Walk both[2] = {fwd, bwd};
+    LinPass& dq = both[0].p;                    // its state is S^T
+    dq.x = d_o; dq.y = v; dq.z = k; dq.u = q; dq.dots = floats(b.qdq);
+    dq.init = a.initial_state; dq.fin = fin; dq.state_t = 1; both[0].joint_t = 1;
+    dq.out = a.dq; dq.out_rep = rep; dq.acc = floats(b.acc);
+    LinPass& dk = both[1].p;                    // dS^T
+    dk.x = v; dk.y = d_o; dk.z = q; dk.u = k; dk.dots = floats(b.kdk);
+    dk.init = a.d_final_state; dk.state_t = 1; both[1].joint_t = 1;
+    dk.out = a.dk; dk.out_rep = rep; dk.acc = floats(b.pair ? b.acc2 : b.acc);
+    if (b.pair) {
+        if ((e = launch_walk<kExact, 2>(both, chain)) != cudaSuccess) return e;
+    } else if ((e = launch_walk<kExact, 1>(both, chain)) != cudaSuccess ||
+               (e = launch_walk<kExact, 1>(both + 1, chain)) != cudaSuccess) {
+        return e;
+    }
+    Walk w = bwd;                               // dv: dS
     w.p.x = k; w.p.y = q; w.p.z = d_o;
     w.p.init = a.d_final_state; w.p.fin = a.d_initial_state;
     w.p.out = a.dv;
-    if ((e = launch_walk<kOut>(w, chain)) != cudaSuccess) return e;
+    if ((e = launch_walk<kOut, 1>(&w, chain)) != cudaSuccess) return e;
     double* sums = a.ldg ? nullptr : reinterpret_cast<double*>(ws + b.sums);
     fwd.p.init = a.initial_state;
     const DgArgs dg{floats(b.qdq), floats(b.kdk), bwd.joint, fin, a.d_final_state, a.d_initial_state, a.dg, sums};

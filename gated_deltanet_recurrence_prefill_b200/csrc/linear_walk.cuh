@@ -92,6 +92,19 @@ struct Walk {
     int32_t n_inner;                // upper bound of the number of parts that are not the last
 };
 
+// Passes of one launch: the backward's two of a kind are independent of each other, and short sequences do not fill
+// the GPU with one of them (a scan takes the pair too).  Kernels of their own for one pass and for two: an index into
+// the parameters, where there is only one, costs the dq and dk passes 25%.
+struct WalkPair {
+    Walk w[2];
+};
+template <int kPasses>
+struct Passes {
+    CUtensorMap x[kPasses], y[kPasses], z[kPasses], u[kPasses], out[kPasses];
+    Walk w[kPasses];
+    int32_t blocks;                 // of each pass
+};
+
 struct Part {
     int64_t t0, t1;                 // its tokens
     int32_t seq;                    // -1: there is no such part
@@ -1060,18 +1073,19 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
     }
 }
 
-template <int kMode>
+template <int kMode, int kPasses>
 __global__ void __launch_bounds__(kThreads, 1)
-lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
-                const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mu,
-                const __grid_constant__ CUtensorMap mo, const __grid_constant__ Walk w) {
+lin_walk_kernel(const __grid_constant__ Passes<kPasses> passes) {
     using L = Layout<kMode>;
+    const int which = kPasses == 2 && (int32_t)blockIdx.x >= passes.blocks ? 1 : 0;
+    const unsigned block = blockIdx.x - (unsigned)which * passes.blocks;       // of its pass
+    const Walk& w = passes.w[which];
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t base = smem_u32(sm);
     const int warp = threadIdx.x >> 5;
     const int heads = kMode == kState ? w.p.Hv : w.p.Hv / w.p.out_rep;
-    const int32_t index = (int32_t)(blockIdx.x / heads);
+    const int32_t index = (int32_t)(block / heads);
     // (well before any CTA can have waited long enough to raise it)
     if (w.opens && blockIdx.x == 0 && threadIdx.x == 0) *w.err = 0u;
     if (w.part_seq) grid_wait();                // the lists come from a kernel before
@@ -1117,7 +1131,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     grid_wait();
     grid_next();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + L::kMisc);
-    const int head = (int)(blockIdx.x - (unsigned)index * heads);
+    const int head = (int)(block - (unsigned)index * heads);
     const int reps = kMode == kState ? 1 : w.p.out_rep;
     const Ctx c{w, sm, base, tmem, abort, base + L::kMisc + 8, part, (int32_t)((part.t1 - part.t0 + kC - 1) / kC), head, reps, head * reps};
     if (warp < 8) {
@@ -1125,7 +1139,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         state_role<kMode>(c);
     } else if (warp < 16) {
         regs_dec<kRegsOut>();
-        if (L::kOuts) out_role<kMode>(c, &mo);
+        if (L::kOuts) out_role<kMode>(c, &passes.out[which]);
         else if (warp == 8) decay_role<kMode>(c, 1, 2);
         bulk_wait();                            // rows still leaving (a role that gave up)
     } else if (warp < 20) {
@@ -1136,7 +1150,7 @@ lin_walk_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         else score_role<kMode>(c);
     } else {
         regs_dec<kRegsRest>();
-        if (warp == 24) load_role<kMode>(c, &mx, &my, &mz, &mu);
+        if (warp == 24) load_role<kMode>(c, &passes.x[which], &passes.y[which], &passes.z[which], &passes.u[which]);
         if (warp == 25) kv_role<kMode>(c, 0);
         if (warp == 26 && L::kOuts) out_products_role<kMode>(c);
         if (warp == 26 && kMode == kState) kv_role<kMode>(c, 1);
