@@ -53,7 +53,8 @@ int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, i
 int32_t part_count(int32_t n_seq, int64_t T, int32_t part_len) { return (int32_t)(T / part_len) + n_seq; }
 
 // Turns each part's own sum into its starting state: start' = decay * start + own along the parts of a
-// sequence, in the pass's direction, from init.  One CTA per (sequence, head, 1024 elements).
+// sequence, in the pass's direction, from init.  One CTA per (sequence, head, 1024 elements).  Bound by the latency
+// of its loads, four parts' at a time (9 parts of 48 heads: 7.5 us, the sums still in L2).
 constexpr int kScanThreads = 256;
 constexpr int kScanSeqs = 32;                  // sequences at a time
 
@@ -154,7 +155,8 @@ lin_parts_kernel(const __grid_constant__ Walk w, int32_t* part_seq, int32_t* inn
 // the first term at the part's end from the joints (or the final state), the sums in 64 bits from the last
 // token back.  The sum at the part's first token is known too, <S, dS> in front of it: what the float32 errors of
 // r and c have added up to by then is taken back in proportion to the tokens summed, which leaves about 0.6 of the
-// error (a random walk tied down at both ends).  One CTA per (part, head).
+// error (a random walk tied down at both ends).  One CTA per (part, head).  Bound by the chain of its blocks' sums (8,192
+// tokens of 48 heads: 26 us).
 constexpr int kDgThreads = 256;
 
 GDN_DEVICE double block_sum(double x, double* sm) {
@@ -265,7 +267,7 @@ __global__ void lin_dg_sum_kernel(const double* part_sum, int32_t n_parts, int32
 }
 
 // acc [tokens, width] in float32 -> out in bf16, for the tokens that sequences own; 8 elements a thread.  blockIdx.y:
-// which of two
+// which of two.  Bound by HBM (8,192 tokens x 2,048: 16 us, half of what it reads still in L2)
 struct Rounds {
     const float* acc[2];
     uint16_t* out[2];

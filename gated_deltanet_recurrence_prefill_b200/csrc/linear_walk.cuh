@@ -14,14 +14,18 @@
 //     KV     = (w z)^T y          A operand from TMEM: three bf16 parts
 //     inter  = A x^T              A operand from TMEM: A in bf16 (one part, or three)
 //     P      = x y^T              both from shared memory as TMA left them
-//     intra  = z^T (Gamma o P)^T  z from shared memory, the scores written there (one part, or three)
+//     intra  = z^T (Gamma o P)^T  z from shared memory, the scores written there (two parts, or three)
 //
 // Precision.  w z is split into three bf16 parts (8 bits each: exact), and the
 // state is accumulated in float32 registers from one chunk's KV at a time, so
-// the state is exact to float32 rounding.  Where only out is wanted, A and the
-// scores enter their product rounded to bf16 (2^-8 relative); the passes whose
-// dot products give the decays' gradient (kExact) take three parts of both,
-// because that gradient is a difference of sums that nearly cancel.
+// the state is exact to float32 rounding.  Where only out is wanted, A enters its
+// product rounded to bf16 (2^-9 relative, 128 independent roundings a sum) and the
+// scores in two parts (2^-16): one score's rounding would be that of a whole row
+// of out, and with few tokens nothing averages it (in one part, the error of a
+// short call against 64 bits rose from 1.4 to 1.6 times that of out's own
+// rounding).  The passes whose dot products give the decays' gradient (kExact)
+// take three parts of both, because that gradient is a difference of sums that
+// nearly cancel.
 //
 // Work split.  The state chain runs along a sequence, so a sequence is cut into
 // parts of L tokens: a first launch (kState) gives each part's own sum of KV, a
@@ -40,8 +44,11 @@
 //   warp  27     the chunk's decays; it waits for every stage to come round, and for
 //                the other roles to end, at most two seconds each, and makes every
 //                other wait give up when that is over (the error word is raised)
-// What bounds it is issue slots (2,200 instructions a chunk and scheduler) and the
-// hand-overs between the roles, so:
+// Measured (8,192 tokens, 16 / 48 heads, float32 state): kState 47 us, kOut 105 us
+// (3,500 cycles a chunk; the tensor pipe 36%, HBM 28%, issue slots 59% busy), kExact
+// 193 us (6,400 cycles; 27%, 46%, 54%); a prefill 141 us, of 65,536 tokens 970 us,
+// a backward 657 us.  What bounds it is issue slots (2,000 instructions a chunk and
+// scheduler) and the hand-overs between the roles, so:
 //  - w z and u are read, and the output is written, as transposed 8 x 8 matrices
 //    (ldmatrix / stmatrix), whose fragments are those of TMEM's 16-lane shapes; with
 //    two-byte accesses the shared-memory pipe took 16 cycles each (7,300 cycles a chunk);
@@ -174,7 +181,8 @@ static_assert(2 * kRegsState + 2 * kRegsOut + 72 + kRegsScores + kRegsRest <= 7 
 template <int kMode>
 struct Layout {
     static constexpr bool kOuts = kMode != kState;
-    static constexpr int kParts = kMode == kExact ? 3 : 1;         // of A and of the scores
+    static constexpr int kParts = kMode == kExact ? 3 : 1;         // of A
+    static constexpr int kScoreParts = kMode == kExact ? 3 : 2;
     // shared memory: stages of [x twice] y z [u] tiles, the scores, decays per stage, barriers
     static constexpr uint32_t kX = 0;                              // per panel: 64 rows, and the same again
     static constexpr uint32_t kY = kOuts ? 2 * kTile : 0;
@@ -187,7 +195,7 @@ struct Layout {
     static constexpr uint32_t kRows = 32 * 128, kHalf = 4 * kRows;
     static_assert(!kOuts || 2 * kHalf <= kZ, "the output's rows");
     static constexpr uint32_t kScores = kStages * kStage;
-    static constexpr uint32_t kGates = kScores + (kOuts ? kParts * kPanel : 0);
+    static constexpr uint32_t kGates = kScores + (kOuts ? kScoreParts * kPanel : 0);
     // a stage's decays: a[64], w[64], exponent high and low [64] each, gamma, tokens
     static constexpr uint32_t kGateBytes = (4 * 64 + 4) * 4;
     static constexpr uint32_t kDots = kGates + kStages * kGateBytes;       // [2][8 warps][32] partial dot products
@@ -251,6 +259,14 @@ GDN_DEVICE void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
     hi = __byte_perm(b0, b1, 0x7632);
     mid = __byte_perm(m0, m1, 0x7632);
     lo = pack_bf16x2(l.x, l.y);
+}
+
+// x = hi + lo in bf16, the rest below 2^-16 of x
+GDN_DEVICE void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+    const uint32_t b0 = __float_as_uint(x.x), b1 = __float_as_uint(x.y);
+    const float2 r = sub2(x, make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)));
+    hi = __byte_perm(b0, b1, 0x7632);
+    lo = pack_bf16x2(r.x, r.y);
 }
 
 // ex2.approx keeps 2^-22 relative; exponents here are <= 0
@@ -560,11 +576,11 @@ GDN_DEVICE void out_products_role(const Ctx& c) {
             tc_fence_after();
             const uint64_t dz = mn_major<kMode>(c, st, L::kZ);
 #pragma unroll
-            for (int part = L::kParts - 1; part >= 0; --part)
+            for (int part = L::kScoreParts - 1; part >= 0; --part)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16(c.tmem + L::tP + set, dz + kk * 128, dScores + part * (kPanel >> 4) + kk * 2, idPv,
-                             part < L::kParts - 1 || kk > 0);
+                             part < L::kScoreParts - 1 || kk > 0);
             commit_to(c, L::kBars, L::bOFull);
             commit_to(c, L::kBars, L::bEmpty + st);
             ring.next();
@@ -682,7 +698,7 @@ GDN_DEVICE void score_role(const Ctx& c) {
         if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
         const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
         const int valid = reinterpret_cast<const int32_t*>(gate)[257];
-        // (kExact: the exponents' high and low parts; else one number, whose rounding is far below bf16's)
+        // (kExact: the exponents' high and low parts; else one number, whose rounding is far below that of the state's copy)
         const float eh = gate[128 + t], el = gate[192 + t];
         const float2 eh2 = make_float2(eh, eh), el2 = make_float2(el, el);
         // the scores of the chunk before have been used
@@ -692,7 +708,7 @@ GDN_DEVICE void score_role(const Ctx& c) {
         uint8_t* row = c.sm + L::kScores;
         if (!two) {
 #pragma unroll
-            for (int k = 0; k < L::kParts; ++k)
+            for (int k = 0; k < L::kScoreParts; ++k)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     *reinterpret_cast<uint4*>(row + k * kPanel + sw128_off(t, empty / 8 + j)) = make_uint4(0u, 0u, 0u, 0u);
@@ -725,10 +741,10 @@ GDN_DEVICE void score_role(const Ctx& c) {
                 for (int e = 0; e < 4; ++e) {
                     const float2 x = make_float2(p[8 * j + 2 * e], p[8 * j + 2 * e + 1]);
                     if (kMode == kExact) split3(x, v[0][e], v[1][e], v[2][e]);
-                    else v[0][e] = pack_bf16x2(x.x, x.y);
+                    else split2(x, v[0][e], v[1][e]);
                 }
 #pragma unroll
-                for (int k = 0; k < L::kParts; ++k)
+                for (int k = 0; k < L::kScoreParts; ++k)
                     *reinterpret_cast<uint4*>(row + k * kPanel + sw128_off(t, s / 8 + j)) =
                         make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
             }

@@ -642,7 +642,8 @@ size_t gdn_linear_prefill_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, 
  *  workspace      gdn_linear_prefill_workspace_size() bytes, 256-byte aligned;
  *                 calls that share it must be ordered on one stream.
  * The final state is exact to float32 rounding; o carries the rounding to bf16 of
- * the score matrix and of the state that the tokens meet (relative 2^-8 each).
+ * the state that the tokens meet (2^-9 of each of its elements) and, with o_bf16,
+ * its own.
  * Errors as for gdn_prefill.
  */
 gdn_status gdn_linear_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t ldq, int64_t ldk,
@@ -666,8 +667,8 @@ size_t gdn_linear_prefill_backward_workspace_size(int32_t n_seq, int64_t T, int3
  *  d_initial_state [n_seq, Hv, d_v, d_k] float32 or NULL (not written); may not be
  *                 d_final_state or initial_state.
  * No atomics: the result is deterministic.  dg and d_initial_state are exact to
- * float32 rounding; dq, dk and dv as o in the prefill.  A log decay at or below
- * -104 has gradient 0.
+ * float32 rounding, as are dq and dk before their own; dv is as o in the prefill.
+ * A log decay at or below -104 has gradient 0.
  */
 gdn_status gdn_linear_prefill_backward(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t ldq,
                                        int64_t ldk, int64_t ldv, const float* g, int32_t g_per_token,
