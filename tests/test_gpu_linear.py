@@ -501,3 +501,74 @@ def test_workspace_reports_no_timeout():
     ws = torch.full((gdn.linear_prefill_workspace_size(1, 300, 1, 1),), 255, dtype=torch.uint8, device="cuda")
     gdn.linear_prefill(q, k, v, g, workspace=ws)
     assert gdn.prefill_status(ws) == 0
+
+
+def test_scores_of_short_sequences():
+    """Without a state in front only the scores matter: two bf16 parts keep 2^-16 of each (m); the 128 products of a
+    score are added in float32, at most 128 x 2^-23 = 2^-16 of their magnitudes (m_abs), the decay, the sum over at most
+    64 tokens and the scale less than as much again.  Scores rounded once to bf16 are off by up to 2^-9 of m."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    c = Case(51, [1, 3, 17, 0, 64, 2], 2, 4, init=False)
+    q, k, v, g = c.dev()
+    o, _ = gdn.linear_prefill(q, k, v, g, cu_seqlens=dev_i32(c.cu), scale=c.scale, o_dtype=torch.float32)
+    want = ref.prefill(c.q, c.k, c.v, c.gr, c.cu, c.scale)[0]
+    m, _ = ref.sizes(c.q, c.k, c.v, c.gr, c.cu, c.scale)
+    m_abs, _ = ref.sizes(*(np.abs(x) for x in (c.q, c.k, c.v)), c.gr, c.cu, c.scale)
+    close(o, want, 2.0 ** -16 * m + 2.0 ** -15 * m_abs + 1e-30, "o")
+
+
+def test_rows_but_no_tokens():
+    """Sequences that are all empty, with rows behind them."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    c = Case(52, [0, 0, 0], 1, 2, per_head=True, tail=150)
+    q, k, v, g = c.dev()
+    cu, s0, dfin = dev_i32(c.cu), dev_f32(c.s0), dev_f32(c.dfin)
+    o = torch.full((150, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, fin = gdn.linear_prefill(q, k, v, g, cu_seqlens=cu, initial_state=s0, o=o)
+    assert torch.equal(fin, s0) and (o == 7.0).all()
+    out = {n: torch.full((150, h, D), 7.0, device="cuda") for n, h in (("dq", 1), ("dk", 1), ("dv", 2))}
+    r = gdn.linear_prefill_backward(q, k, v, g, dev_bf16(c.dob), d_final_state=dfin, cu_seqlens=cu, initial_state=s0,
+                                    out=out)
+    assert torch.equal(r["d_initial_state"], dfin) and not r["dg"].any()
+    assert all((r[n] == 7.0).all() for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("lengths,Hqk,Hv", [([90], 2, 4), ([70, 0, 131, 64, 1], 16, 32)], ids=["together", "in turn"])
+@pytest.mark.parametrize("g16", [True, False])
+def test_backward_passes_together_and_in_turn(lengths, Hqk, Hv, g16):
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    c = Case(53, lengths, Hqk, Hv)
+    q, k, v, g = c.dev(True)
+    r = gdn.linear_prefill_backward(q, k, v, g, dev_bf16(c.dob), d_final_state=dev_f32(c.dfin), cu_seqlens=dev_i32(c.cu),
+                                    scale=c.scale, initial_state=dev_f32(c.s0),
+                                    grad_dtype=torch.bfloat16 if g16 else torch.float32)
+    check_backward(c, r, g16)
+
+
+@pytest.mark.parametrize("lengths", [[300], [6000], [170] * 39 + [3000]], ids=["whole", "in parts", "listed"])
+def test_one_workspace_for_call_after_call(lengths):
+    """Calls that follow one another on a stream share a workspace, whatever it held; its error word ends clear."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    cases = [Case(60 + i, lengths, 1, 2) for i in range(2)]
+    size = max(gdn.linear_prefill_workspace_size(len(lengths), sum(lengths), 1, 2),
+               gdn.lib().gdn_linear_prefill_backward_workspace_size(len(lengths), sum(lengths), 1, 2, D))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    dev = [(c.dev(), dev_bf16(c.dob), dev_i32(c.cu), dev_f32(c.s0), dev_f32(c.dfin)) for c in cases]
+
+    def run(d, workspace):
+        o, fin = gdn.linear_prefill(*d[0], cu_seqlens=d[2], initial_state=d[3], workspace=workspace)
+        r = gdn.linear_prefill_backward(*d[0], d[1], cu_seqlens=d[2], initial_state=d[3], d_final_state=d[4],
+                                        workspace=workspace)
+        return [o, fin] + [r[n] for n in ("dq", "dk", "dv", "dg", "d_initial_state")]
+    alone = []
+    for d in dev:
+        alone.append(run(d, None))
+        torch.cuda.synchronize()
+    for _ in range(3):
+        for got, want in zip([run(d, ws) for d in dev], alone):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert gdn.prefill_status(ws) == 0
