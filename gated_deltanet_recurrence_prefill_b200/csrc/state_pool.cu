@@ -26,16 +26,19 @@ GDN_DEVICE void cp_async16(uint32_t dst, const void* src) {
 // brings the range of all sources into shared memory and then writes it to all
 // destinations, so every read of the range comes before every write of it, and
 // no two items touch the same bytes.  No second cache and no order of moves is
-// needed, and each page is read once and written once.  57 pages of 75 MB (and
-// their conv histories) from 36: 4.9 TB/s, with one item at a time 4.4.
-constexpr int kCopyThreads = 512;
-constexpr int kCopyStage = 48 * 1024;          // bytes of an item; a CTA has room for two, an SM for two CTAs
-constexpr int kCopyCtas = 2;
-constexpr int kCopyMinRange = 64;              // least bytes of a page in an item (1,024 entries: 128 KB of room)
-constexpr int kCopyMostSmem = kMaxStateCopies * (2 * kCopyMinRange + 8);
-static_assert(kCopyMostSmem >= 2 * kCopyStage + 8 * (kCopyStage / kCopyMinRange), "the most that any number of entries takes");
+// needed, and each page is read once and written once.  Bound by HBM, whose rate
+// falls where reads and writes of short ranges take turns: 57 pages of 75 MB (and
+// their conv histories) from 36, 6.3 GB in 1.14 ms, 5.5 TB/s, with ranges of 1,792
+// bytes; with half the room, 512 bytes and two CTAs an SM 4.9, with one item at a
+// time 4.4.  384 threads: 512 took 1.16 ms, 640 1.17.
+constexpr int kCopyThreads = 384;
+constexpr int kCopyStage = 104 * 1024;         // bytes of an item; a CTA has room for two, an SM for one CTA
+constexpr int kCopyMostRange = 32 * 1024, kCopyStep = 128, kCopyMinRange = 64;      // bytes of a page in an item
+constexpr int kCopyMostSmem = 2 * kCopyStage + 8 * (kCopyStage / kCopyStep);
+static_assert(kCopyMostSmem >= kMaxStateCopies * (2 * kCopyMinRange + 8) && kCopyMostSmem <= 227 * 1024,
+              "the most that any number of entries takes");
 
-__global__ void __launch_bounds__(kCopyThreads, kCopyCtas)
+__global__ void __launch_bounds__(kCopyThreads, 1)
 state_copy_kernel(StateBuffers b, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int32_t n,
                   int32_t range) {
     extern __shared__ __align__(16) uint8_t sm[];
@@ -299,17 +302,23 @@ size_t state_workspace_bytes(int32_t n_slots) { return (16 + (size_t)n_slots * 8
 
 cudaError_t launch_state_copy(const StateBuffers& b, const int32_t* src, const int32_t* dst, int32_t n,
                               cudaStream_t s) {
-    // the range of a page per item: a power of two, so that an item of all entries fits the stage
-    int range = 16 * 1024;
-    while (range > kCopyMinRange && (int64_t)range * n > kCopyStage) range >>= 1;
-    int64_t items = 0;
+    // The range of a page per item: what fits the room, in whole lines, or less where that would leave SMs without an
+    // item (down to 1 KB); with more than 832 entries half a line.
+    constexpr int kSms = 148;
+    int64_t page = 0, items = 0;
+    for (int k = 0; k < b.n; ++k) page += b.bytes[k];
+    int range = kCopyStage / n / kCopyStep * kCopyStep;
+    if (range > kCopyMostRange) range = kCopyMostRange;
+    const int64_t share = page / kSms / kCopyStep * kCopyStep;
+    if (range > share) range = share > 1024 ? (int)share : range < 1024 ? range : 1024;
+    if (range == 0) range = kCopyMinRange;
     for (int k = 0; k < b.n; ++k) items += (b.bytes[k] + range - 1) / range;
     if (items == 0) return cudaSuccess;
     const size_t smem = 2 * (size_t)n * range + (size_t)n * 8;
     // (one limit for every call: two at once must not lower it for each other)
     cudaError_t e = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopyMostSmem);
     if (e != cudaSuccess) return e;
-    const int64_t grid = items < 148 * kCopyCtas ? items : 148 * kCopyCtas;
+    const int64_t grid = items < kSms ? items : kSms;
     state_copy_kernel<<<(unsigned)grid, kCopyThreads, smem, s>>>(b, src, dst, n, range);
     return cudaGetLastError();
 }
