@@ -864,6 +864,7 @@ GDN_DEVICE void state_role(const Ctx& c) {
         else if (c.w.split && !c.part.alone) load_state(S, c.w.joint + joint, c.w.joint_t != 0, z, half, room);
         else load_state(S, p.init ? p.init + own : nullptr, p.state_t != 0, z, half, room);
         if (kMode == kOut && r == 0) {
+            fence_async_smem();                 // every lane's last access to the room comes before TMA's writes there
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bStateIn));
         }

@@ -1,0 +1,55 @@
+"""The hand-overs between the roles of the linear attention passes, read from their source.
+
+A missing fence shows in no result that a test could compare (the hardware mostly orders what the memory model leaves
+open), so the order is read from the text of linear_walk.cuh, function by function, in the order in which it stands.
+"""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SRC = os.path.join(ROOT, "gated_deltanet_recurrence_prefill_b200", "csrc", "linear_walk.cuh")
+
+
+def functions():
+    """{name: body} of the source's device functions and kernels, without comments."""
+    text = re.sub(r"/\*.*?\*/", "", re.sub(r"//[^\n]*", "", open(SRC).read()), flags=re.S)
+    out = {}
+    for m in re.finditer(r"^(?:GDN_DEVICE [^;{}]*?|lin_walk_kernel)\b(\w+)?\([^;{}]*\)\s*(?:const )?\{", text, re.M):
+        name = re.findall(r"(\w+)\(", m.group(0))[0]
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        out[name] = text[m.end():i - 1]
+    return out
+
+
+BODIES = functions()
+# (function, barrier): what the waiter lets the asynchronous proxy (TMA, the tensor cores) read or overwrite in shared
+# memory, the threads that arrive have written with ordinary stores
+ASYNC_NEXT = [("state_role", "bStateIn"), ("weight_role", "bZeroed"), ("score_role", "bPReady"), ("out_role", "bRows")]
+
+
+def test_all_roles_are_read():
+    assert {"load_role", "decay_role", "kv_role", "out_products_role", "weight_role", "score_role", "put_state",
+            "state_role", "out_role", "lin_walk_kernel"} <= set(BODIES)
+
+
+@pytest.mark.parametrize("role,barrier", ASYNC_NEXT)
+def test_ordinary_stores_are_fenced_before_the_asynchronous_proxy_may_have_the_bytes(role, barrier):
+    """Every thread runs fence.proxy.async between its last ordinary access and the arrival: the fence, then the warp
+    together, then one lane's arrival."""
+    body = BODIES[role]
+    arrivals = list(re.finditer(r"mbar_arrive\(c\.bar\(L::kBars, L::%s\b[^;]*;" % barrier, body))
+    assert arrivals
+    for a in arrivals:
+        before = body[:a.start()]
+        sync = before.rindex("__syncwarp()")
+        assert re.fullmatch(r"__syncwarp\(\);\s*if \(lane == 0\) \{?\s*", before[sync:]), "the warp, then one lane"
+        fence = before.rfind("fence_async_smem()")
+        assert fence >= 0, f"{role} arrives on {barrier} without a proxy fence"
+        between = before[fence:sync]
+        assert not re.search(r"\*reinterpret_cast|load_state|store_state|clear_rows|stmatrix|ldmatrix", between)
+
