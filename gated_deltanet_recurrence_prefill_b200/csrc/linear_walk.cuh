@@ -897,7 +897,10 @@ GDN_DEVICE void state_role(const Ctx& c) {
                 }
                 ring.next();
                 // inter has read the copy for the chunk before
-                if (L::kOuts && !c.wait(L::kBars, L::bOFull, it)) return;
+                if (L::kOuts) {
+                    if (!c.wait(L::kBars, L::bOFull, it)) return;
+                    tc_fence_after();
+                }
                 ++it;
             }
             if (L::kOuts && n < c.chunks) put_state<kMode>(c, lanes, half, S);
@@ -1191,6 +1194,7 @@ lin_walk_kernel(const __grid_constant__ Passes<kPasses> passes) {
         w.joint_decay[(int64_t)part.slot * w.p.Hv + head] =
             exp2f((float)((double)(sum[0] + sum[1]) * (1.0 / 4294967296.0))) + bad[0] + bad[1];
     }
+    tc_fence_after();
     if (warp == 25) tmem_dealloc(tmem, 512);
 }
 

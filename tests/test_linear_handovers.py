@@ -53,3 +53,22 @@ def test_ordinary_stores_are_fenced_before_the_asynchronous_proxy_may_have_the_b
         between = before[fence:sync]
         assert not re.search(r"\*reinterpret_cast|load_state|store_state|clear_rows|stmatrix|ldmatrix", between)
 
+
+TMEM = re.compile(r"c\.wait\(|wait_set<|tc_fence_after\(\)|\btmem_(?:ld|st)\w*\(|\bput_state<|\bmma_bf16\w*\(|\bscores\(|"
+                  r"__syncthreads\(\)|\btmem_dealloc\(")
+
+
+@pytest.mark.parametrize("role", ["kv_role", "out_products_role", "weight_role", "score_role", "state_role", "out_role",
+                                  "lin_walk_kernel"])
+def test_tensor_memory_is_touched_behind_a_fence(role):
+    """After a wait tcgen05.fence::after_thread_sync comes before the next tcgen05 operation (tmem_st_wait orders the
+    thread's own stores and needs none)."""
+    waited = False
+    for m in TMEM.finditer(BODIES[role]):
+        what = m.group(0)
+        if "wait(" in what and "tmem" not in what or "wait_set" in what or "syncthreads" in what:
+            waited = True
+        elif "tc_fence_after" in what:
+            waited = False
+        elif what != "tmem_st_wait(":
+            assert not waited, f"{role}: {what} after a wait without tcgen05.fence::after_thread_sync"
