@@ -437,11 +437,14 @@ GDN_DEVICE void decay_role(const Ctx& c, int which, int stride) {
                 whole += ((long long)allH << 22) + allL;
                 whole_bad += bad;
             }
+            // (sums up to a token: a NaN at it or before it; sums behind it: one after it)
             const float bad0 = (((nan0 | nan1) & earlier) | (nan0 & (1u << lane))) ? bad : 0.f;
             const float bad1 = (bad0 != bad0 || (nan1 & (1u << lane))) ? bad : 0.f;
+            const float behind1 = ((nan0 | nan1) & ~earlier & ~(1u << lane)) ? bad : 0.f;
+            const float behind0 = (nan1 & (1u << lane)) ? bad : behind1;
             const float e0 = exp2_fast(high(H0) + low(L0) + bad0), e1 = exp2_fast(high(H1) + low(L1) + bad1);
-            const float f0 = exp2_fast(high(allH - H0) + low(allL - L0) + bad);
-            const float f1 = exp2_fast(high(allH - H1) + low(allL - L1) + bad);
+            const float f0 = exp2_fast(high(allH - H0) + low(allL - L0) + behind0);
+            const float f1 = exp2_fast(high(allH - H1) + low(allL - L1) + behind1);
             // (the bound of all waits of the CTA: a stage comes round within kWaitLimitNs)
             if (it >= L::kStages &&
                 !mbar_wait(c.bar(L::kBars, L::bEmpty + ring.st), ring.phase ^ 1u, c.abort, kWaitLimitNs))
@@ -450,10 +453,12 @@ GDN_DEVICE void decay_role(const Ctx& c, int which, int stride) {
             reinterpret_cast<float2*>(gate)[lane] = make_float2(bw ? f0 : e0, bw ? f1 : e1);
             reinterpret_cast<float2*>(gate + 64)[lane] = make_float2(i0 < valid ? ws * (bw ? e0 : f0) : 0.f,
                                                                      i1 < valid ? ws * (bw ? e1 : f1) : 0.f);
+            // (no NaN here: an out_t whose decays have one gets it from a_t, and the scores between tokens on the same
+            // side of it stay)
             // the exponent of Gamma_ts is E_t - E_s; kExact: high parts (whose differences are exact) and low ones
             const float sg = bw ? -1.f : 1.f;
             const float x0 = kMode == kExact ? high(H0) : high(H0) + low(L0), x1 = kMode == kExact ? high(H1) : high(H1) + low(L1);
-            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * x0 + bad0, sg * x1 + bad1);
+            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * x0, sg * x1);
             if (kMode == kExact) reinterpret_cast<float2*>(gate + 192)[lane] = make_float2(sg * low(L0), sg * low(L1));
             if (lane == 31) {
                 gate[256] = e1;                                 // the whole chunk's decay
