@@ -211,7 +211,7 @@ struct Layout {
     static constexpr int bFull = 0, bEmpty = bFull + kStages, bPFull = bEmpty + kStages, bPReady = bPFull + 1,
                          bAReady = bPReady + 1, bKvFull = bAReady + 1, bKvFree = bKvFull + 2, bOFull = bKvFree + 2,
                          bOFree = bOFull + 1, bWFull = bOFree + 1, bWFree = bWFull + kSlotBufs, bZeroed = bWFree + kSlotBufs,
-                         bRows = bZeroed + 1, bDrain = bRows + 2, bDone = bDrain + 2, bStateIn = bDone + 1,
+                         bRows = bZeroed + 1, bDrain = bRows + 4, bDone = bDrain + 2, bStateIn = bDone + 1,
                          kBarCount = bStateIn + 1;
     static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag, a part's decay
     static constexpr uint32_t kSmem = kMisc + 64;
@@ -1028,14 +1028,16 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
             const bool whole = half * 32 + 32 <= valid;         // every row of this half is this part's
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(c.bar(L::kBars, L::bRows + half));
+                mbar_arrive(c.bar(L::kBars, L::bRows + half + 2 * (int)(it & 1u)));
                 if (whole && quad != 0) mbar_arrive(c.bar(L::kBars, L::bEmpty + st));
             }
             const uint32_t now = it++;
             ring.next();
             if (whole && quad != 0) continue;
-            // the four warps of this half have their z indices in place
-            if (!c.wait(L::kBars, L::bRows + half, now)) return;
+            // The four warps of this half have their z indices in place.  Two barriers in turn: a warp that has not yet
+            // arrived for this chunk has released its products all the same, so the others may arrive for the next one
+            // before it (not for the one after, whose products wait for all of them).
+            if (!c.wait(L::kBars, L::bRows + half + 2 * (int)(now & 1u), now >> 1)) return;
             if (kMode == kExact && quad == 0 && half * 32 + lane < valid) {
                 // (two buffers: the chunk after the next needs this stage, which this warp has not yet released)
                 static_assert(kMode != kExact || L::kStages == 2, "the buffers of the dot products");
@@ -1140,8 +1142,7 @@ lin_walk_kernel(const __grid_constant__ Passes<kPasses> passes) {
             init(L::bWFree + k, 1);
         }
         init(L::bZeroed, kMode == kState ? 8 : 4);
-        init(L::bRows, 4);
-        init(L::bRows + 1, 4);
+        for (int k = 0; k < 4; ++k) init(L::bRows + k, 4);
         init(L::bDrain, 1);
         init(L::bDrain + 1, 1);
         init(L::bDone, 27);

@@ -72,3 +72,75 @@ def test_tensor_memory_is_touched_behind_a_fence(role):
             waited = False
         elif what != "tmem_st_wait(":
             assert not waited, f"{role}: {what} after a wait without tcgen05.fence::after_thread_sync"
+
+
+class Barrier:
+    """An mbarrier: a phase ends with its last arrival."""
+
+    def __init__(self, count):
+        self.count, self.left, self.phase = count, count, 0
+
+    def arrive(self):
+        self.left -= 1
+        if self.left == 0:
+            self.left, self.phase = self.count, self.phase + 1
+
+    def passed(self, parity):                    # what mbarrier.try_wait.parity tells
+        return self.phase & 1 != parity & 1
+
+
+def output_rows(sets, slow, order, chunks=12):
+    """The output's four warps of one half and the thread that issues the products, one step of one of them at a time:
+    `slow` gets a step only when nobody else can take one.  Returns the chunks whose rows warp 0 sent away before all
+    four warps had put theirs in place."""
+    full, free, rows = Barrier(1), Barrier(4), [Barrier(4) for _ in range(sets)]
+    placed, early = [0] * 4, []
+
+    def products():
+        for n in range(chunks):
+            while n > 0 and not free.passed(n - 1):
+                yield False
+            full.arrive()
+            yield True
+
+    def warp(w):
+        for n in range(chunks):
+            while not full.passed(n):
+                yield False
+            free.arrive()                        # its part of the products is read ...
+            yield True
+            placed[w] = n + 1                    # ... and only then are its rows in place
+            yield True
+            rows[n % sets].arrive()
+            yield True
+            if w == 0:
+                while not rows[n % sets].passed(n // sets):
+                    yield False
+                if min(placed) <= n:
+                    early.append(n)
+                yield True
+
+    agents = {"products": products(), **{w: warp(w) for w in range(4)}}
+    while agents:
+        for name in sorted(agents, key=lambda a: (a == slow, order.index(a))):
+            step = next(agents[name], None)
+            if step is None:
+                del agents[name]
+                break
+            if step:
+                break
+        else:
+            raise AssertionError("nobody can take a step")
+    return early
+
+
+def test_the_output_leaves_when_all_warps_have_it_in_place():
+    """Whichever warp falls behind: with the barriers that the source has, and not with one."""
+    layout = re.search(r"bRows = (\w+) \+ 1, bDrain = bRows \+ (\d+),", open(SRC).read())
+    sets = int(layout.group(2)) // 2             # (of each half)
+    names = ["products", 0, 1, 2, 3]
+    found = []
+    for count in (1, sets):
+        found.append([early for slow in names for order in (names, names[::-1]) for early in [output_rows(count, slow, order)]
+                      if early])
+    assert found[0] and not found[1]
