@@ -196,9 +196,12 @@ struct Layout {
     static_assert(!kOuts || 2 * kHalf <= kZ, "the output's rows");
     static constexpr uint32_t kScores = kStages * kStage;
     static constexpr uint32_t kGates = kScores + (kOuts ? kScoreParts * kPanel : 0);
-    // a stage's decays: a[64], w[64], exponent high and low [64] each, gamma, tokens
-    static constexpr uint32_t kGateBytes = (4 * 64 + 4) * 4;
-    static constexpr uint32_t kDots = kGates + kStages * kGateBytes;       // [2][8 warps][32] partial dot products
+    // a stage's decays: a[64], w[64], exponent high and low [64] each, gamma, tokens; 4 flags: z indices 32 i .. of
+    // the chunk have an infinity or NaN, each of them the first token with one in kBad[128] (int32)
+    static constexpr uint32_t kFlags = (4 * 64 + 4) * 4;
+    static constexpr uint32_t kGateBytes = kFlags + 16;
+    static constexpr uint32_t kBad = kGates + kStages * kGateBytes;
+    static constexpr uint32_t kDots = kBad + (kOuts ? kStages * 128 * 4 : 0);       // [2][8 warps][32] partial dot products
     static constexpr uint32_t kBars = kDots + (kMode == kExact ? 2 * 8 * 32 * 4 : 0);
     // the scores, and intra in their place, in one or two sets of columns; KV too
     static constexpr int kPSets = kMode == kOut ? 2 : 1, kKvSets = kMode == kState ? 2 : 1;
@@ -212,7 +215,7 @@ struct Layout {
                          bAReady = bPReady + 1, bKvFull = bAReady + 1, bKvFree = bKvFull + 2, bOFull = bKvFree + 2,
                          bOFree = bOFull + 1, bWFull = bOFree + 1, bWFree = bWFull + kSlotBufs, bZeroed = bWFree + kSlotBufs,
                          bRows = bZeroed + 1, bDrain = bRows + 4, bDone = bDrain + 2, bStateIn = bDone + 1,
-                         kBarCount = bStateIn + 1;
+                         bZDone = bStateIn + 1, kBarCount = bZDone + 4;
     static constexpr uint32_t kMisc = kBars + ((kBarCount * 8 + 15) / 16) * 16;    // TMEM base, abort flag, a part's decay
     static constexpr uint32_t kSmem = kMisc + 64;
     static constexpr uint32_t kAlloc = kSmem + 1024;
@@ -267,6 +270,13 @@ GDN_DEVICE void split2(float2 x, uint32_t& hi, uint32_t& lo) {
     const float2 r = sub2(x, make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)));
     hi = __byte_perm(b0, b1, 0x7632);
     lo = pack_bf16x2(r.x, r.y);
+}
+
+// a b + c for a pair of bf16
+GDN_DEVICE uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
 
 // ex2.approx keeps 2^-22 relative; exponents here are <= 0
@@ -463,6 +473,7 @@ GDN_DEVICE void decay_role(const Ctx& c, int which, int stride) {
             if (lane == 31) {
                 gate[256] = e1;                                 // the whole chunk's decay
                 reinterpret_cast<int32_t*>(gate)[257] = valid;
+                if (L::kOuts) *reinterpret_cast<uint4*>(c.sm + L::kGates + ring.st * L::kGateBytes + L::kFlags) = make_uint4(0u, 0u, 0u, 0u);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bFull + ring.st));
@@ -577,6 +588,9 @@ GDN_DEVICE void out_products_role(const Ctx& c) {
                 for (int kk = 0; kk < 8; ++kk)
                     mma_bf16_ta(c.tmem + L::tInter, c.tmem + L::tA + part * 64 + kk * 8,
                                 dx + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4), idKK, part < L::kParts - 1 || kk > 0);
+            // the weights' warps have looked through z (four barriers in turn: they are at most two chunks ahead, and a phase
+            // passed twice would look like one to come)
+            if (!c.wait(L::kBars, L::bZDone + (it & 3), it >> 2)) break;
             if (!c.wait(L::kBars, L::bPReady, it)) break;
             tc_fence_after();
             const uint64_t dz = mn_major<kMode>(c, st, L::kZ);
@@ -606,6 +620,30 @@ GDN_DEVICE void clear_rows(uint8_t* tile, int valid) {
     for (int i = threadIdx.x & 127; i < (kC - valid) * 16; i += 128)
         *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * kPanel + (valid + (i >> 4)) * 128 + (i & 7) * 16) =
             make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---- infinities and NaN in z ---------------------------------------------------------------------------------
+// A token's z meets the scores of the tokens in front of it too, which are 0, and 0 times an infinity or NaN is not.
+// The weights' warps, which have all of z in their hands, look for them (one bf16 product with 0 per pair: 0 unless one
+// is not finite).  Where a warp finds one among its 32 z indices it leaves zeros in its place, once its weights are
+// made, for intra to read, and the output's warps put NaN into those elements of out from that token on.  The search
+// costs 0.8% of a long prefill and intra's wait for it 1.5%; in the scores' warps it cost 5%, in warp 27 29%, and intra
+// issued without waiting, and again where something was found, 15% (more code in the roles' loops).
+
+// `first`: of each z index the first such token in the pass's direction (past the chunk if there is none)
+GDN_DEVICE void clean_z(uint8_t* tile, int32_t* first, int quad, int lane, int valid, bool bw) {
+    const int z = quad * 32 + lane;
+    int at = bw ? -1 : kC;
+    __syncwarp();                               // every lane's rows have been read
+#pragma unroll 1
+    for (int t = 0; t < valid; ++t) {
+        uint16_t* x = reinterpret_cast<uint16_t*>(tile + (z >> 6) * kPanel + sw128_off(t, (z & 63) >> 3)) + (z & 7);
+        if ((*x & 0x7f80u) == 0x7f80u) {
+            *x = 0;
+            if (bw || at == kC) at = t;
+        }
+    }
+    first[z] = at;
 }
 
 // ---- warps 16-19 (kState: 16-23): w z in three parts ------------------------------------------------------
@@ -643,7 +681,7 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
         }
         const uint32_t tile = c.base + st * L::kStage;
         // 16 tokens x 16 z indices at a time, the next matrices requested before these are worked on
-        uint32_t v[4], next[4];
+        uint32_t v[4], next[4], odd = 0u;
         ldmatrix_x4_trans(tile + at + first * L::kSlot * 128, next);
 #pragma unroll 1
         for (int s = first; s < L::kSlots; s += stride) {
@@ -660,7 +698,10 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
 #pragma unroll
                 for (int hz = 0; hz < 2; ++hz) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) v[m] = next[m];
+                    for (int m = 0; m < 4; ++m) {
+                        v[m] = next[m];
+                        if (L::kOuts) odd = fma_bf16x2(v[m], 0u, odd);
+                    }
                     // (after a slot's last tokens the next slot's, which its first ones are when the stride is 1; past
                     // the chunk's end the first ones again, unused)
                     ldmatrix_x4_trans(tile + (hz ? at : at2) + ((t + 16 * hz) & (kC - 1)) * 128, next);
@@ -678,6 +719,16 @@ GDN_DEVICE void weight_role(const Ctx& c, int first, int stride) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bWFull + buf));
+        }
+        if (L::kOuts) {
+            if (__any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0u)) {
+                clean_z(c.sm + st * L::kStage + L::kZ, reinterpret_cast<int32_t*>(c.sm + L::kBad + st * 512), quad, lane, valid,
+                        c.w.p.backward != 0);
+                if (lane == 0) reinterpret_cast<uint32_t*>(c.sm + L::kGates + st * L::kGateBytes + L::kFlags)[quad] = 1u;
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(c.bar(L::kBars, L::bZDone + (it & 3)));
         }
     }
 }
@@ -919,6 +970,24 @@ GDN_DEVICE void state_role(const Ctx& c) {
     }
 }
 
+// NaN in this warp's staged output, from the first token on whose z is not finite, and in its part of the dot products
+template <int kMode>
+GDN_DEVICE void put_nan(const Ctx& c, int st, int buf, uint32_t rows, int quad, int half, int lane, bool f32) {
+    using L = Layout<kMode>;
+    const bool bw = c.w.p.backward != 0;
+    const int z = quad * 32 + lane, at = reinterpret_cast<const int32_t*>(c.sm + L::kBad + st * 512)[z] - half * 32;
+    uint8_t* to = c.sm + st * L::kStage + rows;
+    __syncwarp();                               // the warp's output is in place
+#pragma unroll 1
+    for (int t = 0; t < 32; ++t) {
+        const bool here = bw ? t <= at : t >= at;
+        if (here && f32) *reinterpret_cast<uint32_t*>(to + quad * L::kRows + sw128_off(t, lane >> 2) + (lane & 3) * 4) = 0x7fc00000u;
+        if (here && !f32) *reinterpret_cast<uint16_t*>(to + (z >> 6) * L::kRows + sw128_off(t, (z & 63) >> 3) + (z & 7) * 2) = 0x7fc0u;
+        if (kMode == kExact && __any_sync(0xffffffffu, here) && lane == 0)
+            reinterpret_cast<uint32_t*>(c.sm + L::kDots)[buf * 256 + (half * 4 + quad) * 32 + t] = 0x7fc00000u;
+    }
+}
+
 // ---- warps 8-15: output -----------------------------------------------------------------------------------------
 // Warp (quad, half): z indices 32 quad .. + 32, tokens 32 half .. + 32.
 template <int kMode>
@@ -945,6 +1014,7 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
             const int valid = reinterpret_cast<const int32_t*>(gate)[257];
             if (!c.wait(L::kBars, L::bOFull, it)) return;
             const uint32_t set = L::kPSets == 2 ? it & 1u : 0u;
+            const bool bad = reinterpret_cast<const uint32_t*>(gate)[L::kFlags / 4 + quad] != 0u;
             tc_fence_after();
             if (held >= 0 && lane == 0) {       // the chunk before's rows have left its stage
                 bulk_wait_read();
@@ -1024,6 +1094,7 @@ GDN_DEVICE void out_role(const Ctx& c, const CUtensorMap* mo) {
                                                                   2 * (lane & 3) + (lane >> 3)] = k2;
                 }
             }
+            if (bad) put_nan<kMode>(c, st, (int)(it & 1u), rows, quad, half, lane, f32);
             fence_async_smem();
             const bool whole = half * 32 + 32 <= valid;         // every row of this half is this part's
             __syncwarp();
@@ -1147,6 +1218,7 @@ lin_walk_kernel(const __grid_constant__ Passes<kPasses> passes) {
         init(L::bDrain + 1, 1);
         init(L::bDone, 27);
         init(L::bStateIn, 8);
+        for (int k = 0; k < 4; ++k) init(L::bZDone + k, 4);
         *abort = 0;
         fence_mbar_init();
     }

@@ -621,6 +621,10 @@ gdn_status gdn_gated_norm(const float* o, const uint16_t* z, const float* norm_w
  *  g         float32, [T, Hv] (g_per_token = 1) or [Hv] (g_per_token = 0: fixed
  *            decays).  A log decay below -104, -inf included, is taken as -104,
  *            whose decay is 0 in float32: the state is reset.  NaN stays NaN.
+ *  Infinities and NaN: an output whose formula uses one becomes NaN (an infinity
+ *            too; not only where the formula gives one), o, dq, dk, dv and the
+ *            states of every other token, element, head and sequence stay as they
+ *            are.  dg is a sum along a sequence and may be NaN in all of it.
  *  cu_seqlens[n_seq] may be less than T here: the tokens behind the last sequence
  *            are not read and their outputs are left as they were.
  */

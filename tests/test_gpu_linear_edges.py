@@ -13,8 +13,8 @@ D = 128
 
 # ---- infinities and NaN -------------------------------------------------------------------------
 # One bad value at one token.  It reaches the outputs that the formulas compute from it, which are then not finite, and
-# none of the others, which are those of the same call without it.  (dg is exempt: a running sum over the sequence, it may
-# be NaN throughout.)
+# none of the others, which are those of the same call without it: bit for bit, where nothing that they are made of has
+# changed.  (dg is exempt: a running sum over the sequence, it may be NaN throughout.)
 
 LENGTHS = [150, 30, 70]
 
@@ -27,6 +27,79 @@ def outputs(c, q, k, v, g, d_o, dtype):
                                     initial_state=s0, grad_dtype=dtype)
     out = dict(o=o, fin=fin, dq=r["dq"], dk=r["dk"], dv=r["dv"], d0=r["d_initial_state"])
     return {n: x.float().cpu().numpy() for n, x in out.items()}
+
+
+def reached(c, which, m, head, i, out):
+    """{output: the elements that depend on the bad one}: token m of the sequence [t0, t1), value head `head` (its key
+    head), element i."""
+    n = int(np.searchsorted(c.cu, m, "right")) - 1
+    t0, t1 = int(c.cu[n]), int(c.cu[n + 1])
+    rep = c.Hv // c.Hqk
+    kh = head // rep
+    vh = slice(kh * rep, kh * rep + rep) if which in ("q", "k") else head         # the value heads that see it
+    on = {name: np.zeros(x.shape, bool) for name, x in out.items()}
+    now, later, earlier = slice(m, m + 1), slice(m, t1), slice(t0, m + 1)
+    if which == "q":
+        on["o"][now, vh] = True
+        on["dk"][earlier, kh, i] = True
+        on["dv"][earlier, vh] = True
+        on["d0"][n, vh, :, i] = True
+    elif which == "k":
+        on["o"][later, vh] = True
+        on["fin"][n, vh, :, i] = True
+        on["dq"][later, kh, i] = True
+        on["dv"][now, vh] = True
+    elif which == "v":
+        on["o"][later, vh, i] = True
+        on["fin"][n, vh, i] = True
+        on["dq"][later, kh] = True
+        on["dk"][now, kh] = True
+    elif which == "d_o":
+        on["dq"][now, kh] = True
+        on["dk"][earlier, kh] = True
+        on["dv"][earlier, vh, i] = True
+        on["d0"][n, vh, i] = True
+    return on
+
+
+# the token: the first and last of a chunk of a sequence, and some inside, whole chunks and cut ones
+@pytest.mark.parametrize("m", [0, 11, 31, 63, 64, 100, 149, 150, 165, 179, 249])
+@pytest.mark.parametrize("which", ["q", "k", "v", "d_o"])
+@pytest.mark.parametrize("Hqk,Hv", [(2, 2), (1, 3)])
+def test_one_bad_value_reaches_what_depends_on_it_only(which, m, Hqk, Hv):
+    import torch
+    c = Case(300 + m, LENGTHS, Hqk, Hv)
+    q, k, v, g = c.dev()
+    d_o = dev_bf16(c.dob)
+    head, i = Hv - 1, (37 * m + 5) % D
+    for bad, dtype in ((float("nan"), torch.bfloat16), (float("inf"), torch.float32), (-float("inf"), torch.bfloat16)):
+        clean = outputs(c, q, k, v, g, d_o, dtype)
+        x = dict(q=q, k=k, v=v, d_o=d_o)
+        hit = x[which].clone()
+        hit[m, head if which in ("v", "d_o") else head // (Hv // Hqk), i] = bad
+        x[which] = hit
+        got = outputs(c, x["q"], x["k"], x["v"], g, x["d_o"], dtype)
+        on = reached(c, which, m, head, i, got)
+        for name in got:
+            assert not np.isfinite(got[name][on[name]]).any(), (name, bad)
+            assert np.array_equal(got[name][~on[name]], clean[name][~on[name]]), (name, bad)
+
+
+def test_many_bad_values():
+    """Several tokens and elements of a chunk, both signs, at once: each element of o turns at its first one."""
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    c = Case(77, [200], 1, 1)
+    q, k, v, g = c.dev()
+    clean = gdn.linear_prefill(q, k, v, g, scale=c.scale, initial_state=dev_f32(c.s0))[0].float().cpu().numpy()
+    rng = np.random.default_rng(4)
+    first = np.full(D, 200)
+    for _ in range(60):
+        m, i = int(rng.integers(64, 200)), int(rng.integers(0, D))
+        v[m, 0, i] = float(rng.choice([np.nan, np.inf, -np.inf]))
+        first[i] = min(first[i], m)
+    o = gdn.linear_prefill(q, k, v, g, scale=c.scale, initial_state=dev_f32(c.s0))[0].float().cpu().numpy()
+    on = np.arange(200)[:, None] >= first
+    assert not np.isfinite(o[:, 0][on]).any() and np.array_equal(o[:, 0][~on], clean[:, 0][~on])
 
 
 @pytest.mark.parametrize("m", [0, 11, 63, 64, 100, 149, 160])

@@ -29,7 +29,8 @@ def functions():
 BODIES = functions()
 # (function, barrier): what the waiter lets the asynchronous proxy (TMA, the tensor cores) read or overwrite in shared
 # memory, the threads that arrive have written with ordinary stores
-ASYNC_NEXT = [("state_role", "bStateIn"), ("weight_role", "bZeroed"), ("score_role", "bPReady"), ("out_role", "bRows")]
+ASYNC_NEXT = [("state_role", "bStateIn"), ("weight_role", "bZeroed"), ("score_role", "bPReady"), ("score_role", "bClean"),
+              ("out_role", "bRows")]
 
 
 def test_all_roles_are_read():
