@@ -29,8 +29,8 @@ def functions():
 BODIES = functions()
 # (function, barrier): what the waiter lets the asynchronous proxy (TMA, the tensor cores) read or overwrite in shared
 # memory, the threads that arrive have written with ordinary stores
-ASYNC_NEXT = [("state_role", "bStateIn"), ("weight_role", "bZeroed"), ("score_role", "bPReady"), ("score_role", "bClean"),
-              ("out_role", "bRows")]
+ASYNC_NEXT = [("state_role", "bStateIn"), ("weight_role", "bZeroed"), ("weight_role", "bZDone"),
+              ("score_role", "bPReady"), ("out_role", "bRows")]
 
 
 def test_all_roles_are_read():
@@ -48,7 +48,7 @@ def test_ordinary_stores_are_fenced_before_the_asynchronous_proxy_may_have_the_b
     for a in arrivals:
         before = body[:a.start()]
         sync = before.rindex("__syncwarp()")
-        assert re.fullmatch(r"__syncwarp\(\);\s*if \(lane == 0\) \{?\s*", before[sync:]), "the warp, then one lane"
+        assert re.fullmatch(r"__syncwarp\(\);[\s}]*if \(lane == 0\) \{?\s*", before[sync:]), "the warp, then one lane"
         fence = before.rfind("fence_async_smem()")
         assert fence >= 0, f"{role} arrives on {barrier} without a proxy fence"
         between = before[fence:sync]
