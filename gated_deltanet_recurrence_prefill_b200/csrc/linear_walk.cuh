@@ -465,11 +465,11 @@ GDN_DEVICE void decay_role(const Ctx& c, int which, int stride) {
                                                                      i1 < valid ? ws * (bw ? e1 : f1) : 0.f);
             // (no NaN here: an out_t whose decays have one gets it from a_t, and the scores between tokens on the same
             // side of it stay)
-            // the exponent of Gamma_ts is E_t - E_s; kExact: high parts (whose differences are exact) and low ones
+            // the exponent of Gamma_ts is E_t - E_s: high parts, whose differences are exact however far strong decays have
+            // taken them, and low ones
             const float sg = bw ? -1.f : 1.f;
-            const float x0 = kMode == kExact ? high(H0) : high(H0) + low(L0), x1 = kMode == kExact ? high(H1) : high(H1) + low(L1);
-            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * x0, sg * x1);
-            if (kMode == kExact) reinterpret_cast<float2*>(gate + 192)[lane] = make_float2(sg * low(L0), sg * low(L1));
+            reinterpret_cast<float2*>(gate + 128)[lane] = make_float2(sg * high(H0), sg * high(H1));
+            reinterpret_cast<float2*>(gate + 192)[lane] = make_float2(sg * low(L0), sg * low(L1));
             if (lane == 31) {
                 gate[256] = e1;                                 // the whole chunk's decay
                 reinterpret_cast<int32_t*>(gate)[257] = valid;
@@ -754,7 +754,7 @@ GDN_DEVICE void score_role(const Ctx& c) {
         if (!c.wait(L::kBars, L::bFull + st, ring.phase)) return;
         const float* gate = reinterpret_cast<const float*>(c.sm + L::kGates + st * L::kGateBytes);
         const int valid = reinterpret_cast<const int32_t*>(gate)[257];
-        // (kExact: the exponents' high and low parts; else one number, whose rounding is far below that of the state's copy)
+        // the exponents' high and low parts
         const float eh = gate[128 + t], el = gate[192 + t];
         const float2 eh2 = make_float2(eh, eh), el2 = make_float2(el, el);
         // the scores of the chunk before have been used
@@ -776,12 +776,9 @@ GDN_DEVICE void score_role(const Ctx& c) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
                 const float4 sh = *reinterpret_cast<const float4*>(gate + 128 + s + j);
-                float2 d0 = add2(eh2, make_float2(-sh.x, -sh.y)), d1 = add2(eh2, make_float2(-sh.z, -sh.w));
-                if (kMode == kExact) {
-                    const float4 sl = *reinterpret_cast<const float4*>(gate + 192 + s + j);
-                    d0 = add2(d0, add2(el2, make_float2(-sl.x, -sl.y)));
-                    d1 = add2(d1, add2(el2, make_float2(-sl.z, -sl.w)));
-                }
+                const float4 sl = *reinterpret_cast<const float4*>(gate + 192 + s + j);
+                const float2 d0 = add2(add2(eh2, make_float2(-sh.x, -sh.y)), add2(el2, make_float2(-sl.x, -sl.y)));
+                const float2 d1 = add2(add2(eh2, make_float2(-sh.z, -sh.w)), add2(el2, make_float2(-sl.z, -sl.w)));
                 const float d[4] = {d0.x, d0.y, d1.x, d1.y};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

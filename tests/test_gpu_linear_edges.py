@@ -1,10 +1,11 @@
 """Linear attention with a decay per head where a value that does not count must not show: infinities and NaN at other
-tokens."""
+tokens, decays far below those that matter."""
 import numpy as np
 import pytest
 
-from tests.helpers import dev_bf16, dev_f32, dev_i32
-from tests.test_gpu_linear import Case
+from oracle import linear as ref
+from tests.helpers import dev_bf16, dev_f32, dev_i32, host
+from tests.test_gpu_linear import Case, close
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +124,31 @@ def test_a_nan_decay_reaches_what_depends_on_it_only(m):
         # sums of other decays start elsewhere: an exponent moves by 2^-20 at most, a part of a score by 2^-16
         a, b = got[name][~on[name]], clean[name][~on[name]]
         assert np.abs(a - b).max() <= 2.0 ** -14 * np.abs(b).max(), name
+
+
+# ---- decays ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("every", [2, 3, 7])
+@pytest.mark.parametrize("reset", [-float("inf"), -104.0, -60.0])
+def test_scores_between_resets(every, reset):
+    """Many resets in a chunk take the sum of its log decays far away (64 / 2 of them to -4,800 in base 2, where float32
+    numbers are 2^-11 apart), and the scores of the tokens between two of them, whose decays are ordinary, keep their
+    digits: 2^-16 of each by their two bf16 parts, and as much again for the 128 products, the decay, the sum over the
+    few tokens that count and the scale.  q and k are positive, so that a score is as large as its products'
+    magnitudes.  One rounded exponent a token would be off by up to 2^-12 ln 2 twice, 3e-4 of a score.  (Behind the
+    first chunk of a sequence the state's copy adds half a step of bf16, 2^-8, of what comes from the state: the
+    magnitudes of the whole without those of the chunks by themselves.)"""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    c = Case(500 + every, [64, 50, 128], 2, 4, init=False)
+    q, k, v, g = c.dev()
+    q, k = q.abs(), k.abs()
+    g[::every] = reset
+    g[1::every] = -0.01 - g[1::every].abs() % 0.7
+    o, _ = gdn.linear_prefill(q, k, v, g, cu_seqlens=dev_i32(c.cu), scale=c.scale, o_dtype=torch.float32)
+    gr = np.maximum(host(g), -104.0)
+    want = ref.prefill(host(q), host(k), c.v, gr, c.cu, c.scale)[0]
+    m, _ = ref.sizes(host(q), host(k), c.v, gr, c.cu, c.scale)
+    chunks = np.concatenate([np.arange(a, b, 64) for a, b in zip(c.cu[:-1], c.cu[1:])] + [c.cu[-1:]])
+    alone, _ = ref.sizes(host(q), host(k), c.v, gr, chunks, c.scale)
+    close(o, want, 2.0 ** -15 * m + 2.0 ** -8 * (m - alone) + 1e-30, "o")
