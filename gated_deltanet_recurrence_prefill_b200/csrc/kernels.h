@@ -173,8 +173,10 @@ struct LinearArgs {
     void* o;
     int32_t o_bf16;
     void* workspace;
+    size_t workspace_bytes;        // at least the least bytes; the fastest plan that fits is taken
 };
 size_t linear_prefill_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hv);
+size_t linear_prefill_least_bytes(int32_t n_seq, int64_t T, int32_t Hv);
 cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t stream);
 
 struct LinearBackwardArgs {
@@ -200,8 +202,10 @@ struct LinearBackwardArgs {
     float* dg;
     float* d_initial_state;        // may be NULL
     void* workspace;
+    size_t workspace_bytes;
 };
 size_t linear_backward_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv);
+size_t linear_backward_least_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv);
 cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t stream);
 
 // one token of it for n_seq x layers units (linear_decode.cu)

@@ -89,10 +89,10 @@ gdn_status gdn_linear_prefill(const uint16_t* q, const uint16_t* k, const uint16
     const void* ptrs[] = {q, k, v, g, cu_seqlens, initial_state, final_state, o};
     for (const void* p : ptrs)
         if (!aligned(p, 16)) return GDN_ERR_MISALIGNED;
-    st = check_workspace(workspace, workspace_bytes, gdn::linear_prefill_workspace_bytes(n_seq, T, Hv), 256);
+    st = check_workspace(workspace, workspace_bytes, gdn::linear_prefill_least_bytes(n_seq, T, Hv), 256);
     if (st != GDN_OK) return st;
     gdn::LinearArgs a{q, k, v, ldq, ldk, ldv, g, g_per_token ? Hv : 0, cu_seqlens, n_seq, T, Hqk, Hv, scale,
-                      initial_state, final_state, o, o_bf16, workspace};
+                      initial_state, final_state, o, o_bf16, workspace, workspace_bytes};
     return done(gdn::launch_linear_prefill(a, (cudaStream_t)stream));
 }
 
@@ -122,11 +122,11 @@ gdn_status gdn_linear_prefill_backward(const uint16_t* q, const uint16_t* k, con
     const void* ptrs[] = {q, k, v, g, cu_seqlens, initial_state, d_o, d_final_state, dq, dk, dv, dg, d_initial_state};
     for (const void* p : ptrs)
         if (!aligned(p, 16)) return GDN_ERR_MISALIGNED;
-    st = check_workspace(workspace, workspace_bytes, gdn::linear_backward_workspace_bytes(n_seq, T, Hqk, Hv), 256);
+    st = check_workspace(workspace, workspace_bytes, gdn::linear_backward_least_bytes(n_seq, T, Hqk, Hv), 256);
     if (st != GDN_OK) return st;
     gdn::LinearBackwardArgs a{q, k, v, ldq, ldk, ldv, g, g_per_token ? Hv : 0, cu_seqlens, n_seq, T, Hqk, Hv, scale,
                               initial_state, d_o, d_final_state, dq, dk, dv, grad_bf16, dg, d_initial_state,
-                              workspace};
+                              workspace, workspace_bytes};
     return done(gdn::launch_linear_backward(a, (cudaStream_t)stream));
 }
 

@@ -23,8 +23,10 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 //     walk:    rounds of `heads` CTAs per part over the SMs, each reps * chunks * kWalk + kStart long
 //     states:  where a sequence has several parts, the same over all parts but the last, chunks * kStateStep long,
 //              and the scan
-// in microseconds, measured on B200.  Sequences that turn out longer than a part are cut.
-int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, int64_t most) {
+// in microseconds, measured on B200.  Sequences that turn out longer than a part are cut.  Only lengths for which the
+// workspace suffices (`fits`) count; the longest there is needs the least.
+template <typename Fits>
+int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, int64_t most, const Fits& fits) {
     constexpr double kWalk = 2.1, kStateStep = 0.85, kStart = 5.0, kScan = 8.0;
     const int64_t all = (T + kC - 1) / kC, chunks = (T + n_seq - 1) / n_seq / kC + 1;
     auto rounds = [](int64_t ctas) { return (double)((ctas + kSms - 1) / kSms); };
@@ -42,9 +44,10 @@ int32_t choose_part_len(int32_t n_seq, int64_t T, int32_t heads, int32_t reps, i
         double cost = rounds((int64_t)n_seq * n * heads) * ((double)(l * reps) * kWalk + kStart);
         // (uneven sequences are cut even where their mean is not)
         cost += rounds((int64_t)n_seq * (n > 1 ? n - 1 : 1) * heads * reps) * ((double)l * kStateStep + kStart) + kScan;
-        if (best < 0.0 || cost < best) {
+        const int64_t whole = n == 1 && 2 * l * kC <= most ? 2 * l : l;            // up to twice the mean stays whole
+        if ((best < 0.0 || cost < best) && fits((int32_t)(whole * kC))) {
             best = cost;
-            len = n == 1 && 2 * l * kC <= most ? 2 * l : l;        // up to twice the mean stays whole
+            len = whole;
         }
     }
     return (int32_t)(len * kC);
@@ -409,9 +412,9 @@ struct Joints {
     size_t state_bytes, decay_bytes, list_bytes;
 };
 
-Joints plan_joints(int32_t n_seq, int64_t T, int32_t Hv, int32_t heads, int64_t most) {
+Joints joints_of(int32_t n_seq, int64_t T, int32_t Hv, int32_t part_len) {
     Joints j;
-    j.part_len = choose_part_len(n_seq, T, heads, Hv / heads, most);
+    j.part_len = part_len;
     j.n_parts = part_count(n_seq, T, j.part_len);
     j.n_inner = (int32_t)(T / j.part_len);      // parts that are not the last of their sequence are whole
     j.split = T > j.part_len;
@@ -436,28 +439,32 @@ cudaError_t set_parts(Walk& w, const Joints& j, char* lists, Chain& chain) {
     return chain.launch(false, lin_parts_kernel, 1, kListThreads, 0, w, part_seq, inner, seq_first);
 }
 
+// A call's plan follows from the workspace it is given: the fastest that fits, or the one that needs least.  What that
+// one needs grows with T and n_seq, so a workspace for the largest of several calls serves all of them, which the
+// fastest plans' sizes, taken call by call, would not let it.
 constexpr int64_t kAnyLength = (int64_t)1 << 30;
+constexpr size_t kAnySize = ~(size_t)0;
+
+size_t prefill_bytes(const Joints& j) { return kWsHeaderBytes + j.state_bytes + j.decay_bytes + j.list_bytes; }
+
+Joints prefill_plan(int32_t n_seq, int64_t T, int32_t Hv, size_t workspace_bytes) {
+    const auto fits = [&](int32_t len) { return prefill_bytes(joints_of(n_seq, T, Hv, len)) <= workspace_bytes; };
+    return joints_of(n_seq, T, Hv, choose_part_len(n_seq, T, Hv, 1, kAnyLength, fits));
+}
 
 struct BackwardPlan {
     Joints j;
-    int32_t pair;                   // dq and dk in one launch
-    size_t qdq, kdk, acc, acc2, fin, sums, fwd, bwd, decay_f, decay_b, lists, bytes;
+    size_t qdq, kdk, acc, fin, sums, fwd, bwd, decay_f, decay_b, lists, bytes;
 };
 
-BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
+BackwardPlan backward_layout(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, int32_t part_len) {
     BackwardPlan b;
-    // parts of at most 4096 tokens: the decays' gradient is a running sum along a part
-    b.j = plan_joints(n_seq, T, Hv, Hqk, 4096);
+    b.j = joints_of(n_seq, T, Hv, part_len);
     size_t off = kWsHeaderBytes;
     auto take = [&](size_t bytes) { const size_t at = off; off += up256(bytes); return at; };
     b.qdq = take((size_t)T * Hv * 4);
     b.kdk = take((size_t)T * Hv * 4);
     b.acc = take(Hv > Hqk ? (size_t)T * Hqk * kD * 4 : 0);
-    // Where both fill no more than one round of CTAs, they share it (572 ragged tokens, 24 CTAs each: 100 -> 81 us for
-    // the whole backward).  Beyond that they take turns, with one accumulator and the faster kernel for one pass
-    // (8,192 tokens, 144 CTAs each: 650 us, in one launch 735).
-    b.pair = 2 * (int64_t)b.j.n_parts * Hqk <= kSms;
-    b.acc2 = take(b.pair && Hv > Hqk ? (size_t)T * Hqk * kD * 4 : 0);
     b.fin = take((size_t)n_seq * Hv * kD * kD * 4);
     b.sums = take((size_t)b.j.n_parts * Hv * 8);
     b.fwd = take(b.j.state_bytes);
@@ -469,11 +476,19 @@ BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
     return b;
 }
 
+BackwardPlan backward_plan(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, size_t workspace_bytes) {
+    const auto fits = [&](int32_t len) { return backward_layout(n_seq, T, Hqk, Hv, len).bytes <= workspace_bytes; };
+    // parts of at most 4096 tokens: the decays' gradient is a running sum along a part
+    return backward_layout(n_seq, T, Hqk, Hv, choose_part_len(n_seq, T, Hqk, Hv / Hqk, 4096, fits));
+}
+
 }  // namespace
 
 size_t linear_prefill_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hv) {
-    const Joints j = plan_joints(n_seq, T, Hv, Hv, kAnyLength);
-    return kWsHeaderBytes + j.state_bytes + j.decay_bytes + j.list_bytes;
+    return prefill_bytes(prefill_plan(n_seq, T, Hv, kAnySize));
+}
+size_t linear_prefill_least_bytes(int32_t n_seq, int64_t T, int32_t Hv) {
+    return prefill_bytes(prefill_plan(n_seq, T, Hv, 0));
 }
 
 cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
@@ -482,7 +497,7 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
         const cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
         return e == cudaSuccess ? pass_state(a.initial_state, a.final_state, a.n_seq, a.Hv, s) : e;
     }
-    const Joints j = plan_joints(a.n_seq, a.T, a.Hv, a.Hv, kAnyLength);
+    const Joints j = prefill_plan(a.n_seq, a.T, a.Hv, a.workspace_bytes);
     Walk w{};
     w.joint = reinterpret_cast<float*>(ws + kWsHeaderBytes);
     w.joint_decay = reinterpret_cast<float*>(ws + kWsHeaderBytes + j.state_bytes);
@@ -502,11 +517,14 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, cudaStream_t s) {
 }
 
 size_t linear_backward_workspace_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
-    return backward_plan(n_seq, T, Hqk, Hv).bytes;
+    return backward_plan(n_seq, T, Hqk, Hv, kAnySize).bytes;
+}
+size_t linear_backward_least_bytes(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv) {
+    return backward_plan(n_seq, T, Hqk, Hv, 0).bytes;
 }
 
 cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) {
-    const BackwardPlan b = backward_plan(a.n_seq, a.T, a.Hqk, a.Hv);
+    const BackwardPlan b = backward_plan(a.n_seq, a.T, a.Hqk, a.Hv, a.workspace_bytes);
     char* ws = static_cast<char*>(a.workspace);
     auto floats = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     cudaError_t e;
@@ -542,8 +560,14 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     LinPass& dk = both[1].p;                    // dS^T
     dk.x = v; dk.y = d_o; dk.z = q; dk.u = k; dk.dots = floats(b.kdk);
     dk.init = a.d_final_state; dk.state_t = 1; both[1].joint_t = 1;
-    dk.out = a.dk; dk.out_rep = rep; dk.acc = floats(b.pair ? b.acc2 : b.acc);
-    if (b.pair) {
+    dk.out = a.dk; dk.out_rep = rep;
+    // Where both fill no more than one round of CTAs, they share it (572 ragged tokens, 24 CTAs each: 100 -> 81 us for
+    // the whole backward), and dk's rows are summed where dv's will be written (as large at least: rep > 1).  Beyond
+    // that they take turns, with one accumulator and the faster kernel for one pass (8,192 tokens, 144 CTAs each: 650 us,
+    // in one launch 735).
+    const bool pair = 2 * (int64_t)b.j.n_parts * a.Hqk <= kSms;
+    dk.acc = pair ? static_cast<float*>(a.dv) : floats(b.acc);
+    if (pair) {
         if ((e = launch_walk<kExact, 2>(both, chain)) != cudaSuccess) return e;
     } else if ((e = launch_walk<kExact, 1>(both, chain)) != cudaSuccess ||
                (e = launch_walk<kExact, 1>(both + 1, chain)) != cudaSuccess) {

@@ -630,10 +630,14 @@ gdn_status gdn_gated_norm(const float* o, const uint16_t* z, const float* norm_w
  */
 
 /*
- * gdn_linear_prefill_workspace_size -- bytes of device workspace for
- * gdn_linear_prefill (a multiple of 256, never 0): a header whose first word is
- * the error word that gdn_prefill_status and gdn_check_async read, and the states
- * at the joints of sequences that are worked on in several parts.  Host-only.
+ * gdn_linear_prefill_workspace_size -- bytes of device workspace with which
+ * gdn_linear_prefill works on sequences in as many parts as is fastest (a multiple
+ * of 256, never 0): a header whose first word is the error word that
+ * gdn_prefill_status and gdn_check_async read, and the states at the joints of the
+ * parts.  With less, down to the header's 256 bytes, it takes fewer and longer
+ * parts, with the same results up to rounding.  The size is not monotonous in T or
+ * n_seq, but a workspace of this size also serves every call with no more of
+ * either (and the same heads).  Host-only.
  */
 size_t gdn_linear_prefill_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, int32_t d);
 
@@ -643,8 +647,8 @@ size_t gdn_linear_prefill_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, 
  *  final_state    the same shape or NULL (not written); may be initial_state.  A
  *                 sequence of length 0 hands its initial state on.
  *  o              [T, Hv, d], float32 (o_bf16 = 0) or bf16 (o_bf16 = 1).
- *  workspace      gdn_linear_prefill_workspace_size() bytes, 256-byte aligned;
- *                 calls that share it must be ordered on one stream.
+ *  workspace      gdn_linear_prefill_workspace_size() bytes (or fewer, see there),
+ *                 256-byte aligned; calls that share it must be ordered on one stream.
  * The final state is exact to float32 rounding; o carries the rounding to bf16 of
  * the state that the tokens meet (2^-9 of each of its elements) and, with o_bf16,
  * its own.
@@ -656,7 +660,12 @@ gdn_status gdn_linear_prefill(const uint16_t* q, const uint16_t* k, const uint16
                               const float* initial_state, float* final_state, void* o, int32_t o_bf16,
                               void* workspace, size_t workspace_bytes, gdn_stream_t stream);
 
-/* Bytes of device workspace for gdn_linear_prefill_backward (a multiple of 256, never 0).  Host-only. */
+/*
+ * gdn_linear_prefill_backward_workspace_size -- the same for
+ * gdn_linear_prefill_backward.  What it cannot do without grows with T and n_seq
+ * (more than 256 bytes); a workspace of this size serves every call with no more
+ * of either.  Host-only.
+ */
 size_t gdn_linear_prefill_backward_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, int32_t Hv, int32_t d);
 
 /*

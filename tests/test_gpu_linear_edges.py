@@ -1,11 +1,11 @@
 """Linear attention with a decay per head where a value that does not count must not show: infinities and NaN at other
-tokens, decays far below those that matter."""
+tokens, decays far below those that matter, what a workspace held or was made for."""
 import numpy as np
 import pytest
 
 from oracle import linear as ref
 from tests.helpers import dev_bf16, dev_f32, dev_i32, host
-from tests.test_gpu_linear import Case, close
+from tests.test_gpu_linear import Case, check_backward, check_prefill, close
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,59 @@ def test_scores_between_resets(every, reset):
     chunks = np.concatenate([np.arange(a, b, 64) for a, b in zip(c.cu[:-1], c.cu[1:])] + [c.cu[-1:]])
     alone, _ = ref.sizes(host(q), host(k), c.v, gr, chunks, c.scale)
     close(o, want, 2.0 ** -15 * m + 2.0 ** -8 * (m - alone) + 1e-30, "o")
+
+
+# ---- workspaces -----------------------------------------------------------------------------------
+
+def test_a_workspace_made_for_a_larger_call():
+    """Every shorter call works in it, though one of its own might be larger, and it may hold anything."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    Hqk, Hv, most = 1, 2, [300, 200, 1300, 61]
+    back = gdn.lib().gdn_linear_prefill_backward_workspace_size
+    size = max(gdn.linear_prefill_workspace_size(4, sum(most), Hqk, Hv), back(4, sum(most), Hqk, Hv, D))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    for i, lengths in enumerate([most, [1088], [960, 1], [300, 0, 41, 2], [64], [1]]):
+        check_with(Case(600 + i, lengths, Hqk, Hv), ws, ws)
+
+
+@pytest.mark.parametrize("lengths", [[1100, 40, 300], [4200], [30] * 39 + [1500]], ids=["three", "one", "listed"])
+def test_workspaces_smaller_than_the_fastest_plan_wants(lengths):
+    """The least, and half of what is between it and the full size: other cuts, the same results up to rounding.  A byte
+    less than the least is refused."""
+    import torch
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    c = Case(620, lengths, 1, 2)
+    n, T = len(lengths), sum(lengths)
+    full = gdn.linear_prefill_workspace_size(n, T, 1, 2)
+    most = gdn.lib().gdn_linear_prefill_backward_workspace_size(n, T, 1, 2, D)
+    # what the gradients cannot do without: dot products, dk's or dq's sums, final states, and for parts of 4,096 tokens
+    # their sums of dg, starting states and decays in both directions, and lists
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    parts = n if T <= 4096 else T // 4096 + n
+    split = T > 4096
+    joints = 2 * up(parts * 2 * D * D * 4) + 2 * up(parts * 2 * 4) if split else 0
+    lists = up((parts + T // 4096 + n + 1) * 4) if split and n > 32 else 0
+    least = 256 + 2 * up(T * 2 * 4) + up(T * D * 4) + up(n * 2 * D * D * 4) + up(parts * 2 * 8) + joints + lists
+    assert full > 256 and most > least
+    for share in (0.0, 0.5):
+        pre, back = (int(a + share * (b - a)) // 256 * 256 for a, b in ((256, full), (least, most)))
+        check_with(c, torch.full((pre,), 255, dtype=torch.uint8, device="cuda"),
+                   torch.full((back,), 255, dtype=torch.uint8, device="cuda"))
+    q, k, v, g = c.dev()
+    with pytest.raises(RuntimeError):
+        gdn.linear_prefill_backward(q, k, v, g, dev_bf16(c.dob), cu_seqlens=dev_i32(c.cu),
+                                    workspace=torch.empty(least - 1, dtype=torch.uint8, device="cuda"))
+
+
+def check_with(c, ws_prefill, ws_backward):
+    import gated_deltanet_recurrence_prefill_b200 as gdn
+    q, k, v, g = c.dev()
+    cu, s0 = dev_i32(c.cu), dev_f32(c.s0)
+    o, fin = gdn.linear_prefill(q, k, v, g, cu_seqlens=cu, scale=c.scale, initial_state=s0, workspace=ws_prefill)
+    check_prefill(c, o, fin, True)
+    assert gdn.prefill_status(ws_prefill) == 0
+    r = gdn.linear_prefill_backward(q, k, v, g, dev_bf16(c.dob), d_final_state=dev_f32(c.dfin), cu_seqlens=cu,
+                                    scale=c.scale, initial_state=s0, workspace=ws_backward)
+    check_backward(c, r, True)
+    assert gdn.prefill_status(ws_backward) == 0
