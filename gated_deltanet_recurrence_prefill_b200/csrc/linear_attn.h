@@ -27,7 +27,7 @@ struct LinOperand {
 struct LinPass {
     LinOperand x, y, z;
     LinOperand u;                       // dots[t, h] = u_t . out_t (float32) when dots is given
-    float* dots = nullptr;              // [T, Hv]
+    float* dots = nullptr;              // [Hv, T]
     const float* g = nullptr;           // log decays: row t at g + t * ldg (ldg = 0: one per head)
     int64_t ldg = 0;
     const int32_t* cu = nullptr;        // NULL: one sequence of length T

@@ -563,8 +563,8 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     dk.out = a.dk; dk.out_rep = rep;
     // Where both fill no more than one round of CTAs, they share it (572 ragged tokens, 24 CTAs each: 100 -> 81 us for
     // the whole backward), and dk's rows are summed where dv's will be written (as large at least: rep > 1).  Beyond
-    // that they take turns, with one accumulator and the faster kernel for one pass (8,192 tokens, 144 CTAs each: 650 us,
-    // in one launch 735).
+    // that they take turns, with one accumulator and the faster kernel for one pass (8,192 tokens, 144 CTAs each: in one
+    // launch the whole backward took 735 us for 650).
     const bool pair = 2 * (int64_t)b.j.n_parts * a.Hqk <= kSms;
     dk.acc = pair ? static_cast<float*>(a.dv) : floats(b.acc);
     if (pair) {

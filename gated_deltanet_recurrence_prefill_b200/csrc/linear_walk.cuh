@@ -18,8 +18,9 @@
 //
 // Precision.  w z is split into three bf16 parts (8 bits each: exact), and the
 // state is accumulated in float32 registers from one chunk's KV at a time, so
-// the state is exact to float32 rounding.  Where only out is wanted, A enters its
-// product rounded to bf16 (2^-9 relative, 128 independent roundings a sum) and the
+// the state is exact to float32 rounding.  Where only out is wanted, whatever its
+// type, A enters its product rounded to bf16 (2^-8 relative at most, 1.7e-3 in the
+// mean, 128 independent roundings a sum) and the
 // scores in two parts (2^-16): one score's rounding would be that of a whole row
 // of out, and with few tokens nothing averages it (in one part, the error of a
 // short call against 64 bits rose from 1.4 to 1.6 times that of out's own
@@ -44,11 +45,12 @@
 //   warp  27     the chunk's decays; it waits for every stage to come round, and for
 //                the other roles to end, at most two seconds each, and makes every
 //                other wait give up when that is over (the error word is raised)
-// Measured (8,192 tokens, 16 / 48 heads, float32 state): kState 47 us, kOut 105 us
-// (3,500 cycles a chunk; the tensor pipe 36%, HBM 28%, issue slots 59% busy), kExact
-// 193 us (6,400 cycles; 27%, 46%, 54%); a prefill 141 us, of 65,536 tokens 970 us,
-// a backward 657 us.  What bounds it is issue slots (2,000 instructions a chunk and
-// scheduler) and the hand-overs between the roles, so:
+// Measured (8,192 tokens, 16 / 48 heads, float32 state): kState 44 us, kOut 103 us
+// (the tensor pipe 34%, HBM 29%, issue slots 57% busy), kExact 188 us (26%, 47%,
+// 52%); 65,536 tokens: kOut 730 us, 3,900 cycles a chunk with all that surrounds it.
+// Calls one after another: a prefill 146 us, of 65,536 tokens 1.00 ms (1.16 ms each by
+// itself), a backward 680 us (720).  What bounds it is issue slots (2,000 instructions
+// a chunk and scheduler) and the hand-overs between the roles, so:
 //  - w z and u are read, and the output is written, as transposed 8 x 8 matrices
 //    (ldmatrix / stmatrix), whose fragments are those of TMEM's 16-lane shapes; with
 //    two-byte accesses the shared-memory pipe took 16 cycles each (7,300 cycles a chunk);

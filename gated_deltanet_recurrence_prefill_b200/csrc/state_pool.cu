@@ -26,11 +26,14 @@ GDN_DEVICE void cp_async16(uint32_t dst, const void* src) {
 // brings the range of all sources into shared memory and then writes it to all
 // destinations, so every read of the range comes before every write of it, and
 // no two items touch the same bytes.  No second cache and no order of moves is
-// needed, and each page is read once and written once.  Bound by HBM, whose rate
-// falls where reads and writes of short ranges take turns: 57 pages of 75 MB (and
-// their conv histories) from 36, 6.3 GB in 1.14 ms, 5.5 TB/s, with ranges of 1,792
-// bytes; with half the room, 512 bytes and two CTAs an SM 4.9, with one item at a
-// time 4.4.  384 threads: 512 took 1.16 ms, 640 1.17.
+// needed; a page is written once, and loaded for every entry that reads it (from L2
+// after the first).  Bound by HBM, whose rate falls where reads and writes of short
+// ranges take turns: 57 pages of 77 MB (with their conv histories) from 23, 6.3 GB
+// to move, in 1.14 ms one call after another (5.5 TB/s; 1.24 ms by itself) with
+// ranges of 1,792 bytes; with half the room, 512 bytes and two CTAs an SM 4.9 TB/s,
+// with one item at a time 4.4.  384 threads: 512 took 1.16 ms, 640 1.17.  Pages of
+// their own, 16 MB from 256: 5.1 TB/s, 4 MB from 832 (128 bytes) 4.3, from more
+// (64 bytes) 2.3.
 constexpr int kCopyThreads = 384;
 constexpr int kCopyStage = 104 * 1024;         // bytes of an item; a CTA has room for two, an SM for one CTA
 constexpr int kCopyMostRange = 32 * 1024, kCopyStep = 128, kCopyMinRange = 64;      // bytes of a page in an item

@@ -621,10 +621,11 @@ gdn_status gdn_gated_norm(const float* o, const uint16_t* z, const float* norm_w
  *  g         float32, [T, Hv] (g_per_token = 1) or [Hv] (g_per_token = 0: fixed
  *            decays).  A log decay below -104, -inf included, is taken as -104,
  *            whose decay is 0 in float32: the state is reset.  NaN stays NaN.
- *  Infinities and NaN: an output whose formula uses one becomes NaN (an infinity
- *            too; not only where the formula gives one), o, dq, dk, dv and the
- *            states of every other token, element, head and sequence stay as they
- *            are.  dg is a sum along a sequence and may be NaN in all of it.
+ *  Infinities and NaN: an output whose formula uses one is not finite (in the
+ *            prefill and its gradients it is NaN, also where the formula gives an
+ *            infinity); o, dq, dk, dv and the states of all other tokens, elements,
+ *            heads and sequences stay as they are.  dg is a sum along a sequence
+ *            and may be NaN in all of it.
  *  cu_seqlens[n_seq] may be less than T here: the tokens behind the last sequence
  *            are not read and their outputs are left as they were.
  */
@@ -649,9 +650,9 @@ size_t gdn_linear_prefill_workspace_size(int32_t n_seq, int64_t T, int32_t Hqk, 
  *  o              [T, Hv, d], float32 (o_bf16 = 0) or bf16 (o_bf16 = 1).
  *  workspace      gdn_linear_prefill_workspace_size() bytes (or fewer, see there),
  *                 256-byte aligned; calls that share it must be ordered on one stream.
- * The final state is exact to float32 rounding; o carries the rounding to bf16 of
- * the state that the tokens meet (2^-9 of each of its elements) and, with o_bf16,
- * its own.
+ * The final state is exact to float32 rounding; o, float32 or bf16, carries the
+ * rounding to bf16 of the state that the tokens meet (2^-8 of each of its elements
+ * at most, 1.7e-3 of what comes from it in the mean) and, with o_bf16, its own.
  * Errors as for gdn_prefill.
  */
 gdn_status gdn_linear_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t ldq, int64_t ldk,
@@ -679,9 +680,12 @@ size_t gdn_linear_prefill_backward_workspace_size(int32_t n_seq, int64_t T, int3
  *  dg             float32, shaped as g ([Hv]: summed over all tokens).
  *  d_initial_state [n_seq, Hv, d_v, d_k] float32 or NULL (not written); may not be
  *                 d_final_state or initial_state.
- * No atomics: the result is deterministic.  dg and d_initial_state are exact to
- * float32 rounding, as are dq and dk before their own; dv is as o in the prefill.
- * A log decay at or below -104 has gradient 0.
+ * No atomics: the result is deterministic.  d_initial_state is exact to float32
+ * rounding, as are dq and dk before their own; dv is as o in the prefill.  dg_t is
+ * a sum along the sequence of float32 terms q . dq and k . dk that nearly cancel:
+ * its error is float32 rounding of those terms from t on, not of dg_t, so a token
+ * whose gradient is far smaller than its neighbours' (a strong decay) has their
+ * noise.  A log decay at or below -104 has gradient 0.
  */
 gdn_status gdn_linear_prefill_backward(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t ldq,
                                        int64_t ldk, int64_t ldv, const float* g, int32_t g_per_token,
@@ -737,7 +741,7 @@ typedef struct gdn_state_buffer {
  *  src, dst  [n] int32 (device), n <= GDN_MAX_STATE_COPIES.  Entries with an index
  *            outside [0, n_slots) are ignored; of several entries with one
  *            destination the last holds.
- * Each page is read and written once; no workspace.
+ * A page is written once and read for each entry that names it; no workspace.
  */
 gdn_status gdn_state_copy(const gdn_state_buffer* buffers, int32_t n_buffers, int32_t n_slots, const int32_t* src,
                           const int32_t* dst, int32_t n, gdn_stream_t stream);
